@@ -14,6 +14,11 @@ Entry points (same names as the C ABI in include/infini_attn.h):
     infini_attn_backward(q, k, v, beta, N, mode, dout, M_in=None, z_in=None, ...)
     infini_attn_layer_forward(x, Wq, Wk, Wv, Wo, beta, N, mode, H, H_kv, ...)
     infini_attn_gemm_bf16(A, B)
+and, in block.py, the operators around the layer:
+    infini_attn_linear(x, W, bias=None, act=ACT_NONE, residual=None, ...), _backward
+    infini_attn_norm(x, weight, bias=None, ...), _backward
+    infini_attn_residual_norm(x, b, gate=None, alpha=1.0, ...), _backward
+    infini_attn_block_forward(x, Wq, Wk, Wv, Wo, beta, N, mode, H, W_up, W_down, ...)
 q, k, v: [B, H, L, d] CUDA tensors, bf16 (d = 128) or fp32 (d <= 128);
 beta: [H] fp32; M: [B, H, d, d] fp32; z: [B, H, d] fp32.
 """
@@ -84,9 +89,6 @@ _lib.infini_attn_strerror.restype = ctypes.c_char_p
 _lib.infini_attn_workspace_size.restype = ctypes.c_size_t
 _lib.infini_attn_backward_workspace_size.restype = ctypes.c_size_t
 _lib.infini_attn_layer_workspace_size.restype = ctypes.c_size_t
-
-# every symbol the header declares (checked by the CPU tests)
-EXPORTED = tuple(_SIGS)
 
 
 class InfiniError(RuntimeError):
@@ -425,3 +427,15 @@ def selftest_timeout(timeout_ns: int, stream=None) -> None:
 def raw_call(name, *args):
     """Call an exported C function by name with ctypes-compatible arguments."""
     return getattr(_lib, name)(*args)
+
+
+from .block import (ACT_GELU, ACT_GELU_TANH, ACT_NONE, ACT_RELU, ACT_SILU,  # noqa: E402,F401
+                    NORM_LAYER, NORM_RMS, ResidualNormGrads, block_workspace_size,
+                    infini_attn_block_forward, infini_attn_linear, infini_attn_linear_backward,
+                    infini_attn_norm, infini_attn_norm_backward, infini_attn_residual_norm,
+                    infini_attn_residual_norm_backward, linear_backward_workspace_size,
+                    residual_norm_backward_workspace_size)
+from .block import SIGS as _BLOCK_SIGS  # noqa: E402
+
+# every symbol the header declares (checked by the CPU tests)
+EXPORTED = (*_SIGS, *_BLOCK_SIGS)

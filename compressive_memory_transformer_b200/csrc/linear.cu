@@ -1,0 +1,508 @@
+// linear.cu — matrix products with a fused epilogue, bf16 in and out, fp32 accumulation
+// on the tensor cores: out = act(A B + bias) + residual, optionally with the
+// pre-activation A B + bias beside it. Either operand may be stored along or across the
+// reduction (the tensor cores read both from shared memory, K-major or MN-major), so one
+// set of kernels serves the forward product x W and the gradients dpre W^T and x^T dpre
+// without a transposed copy of anything.
+//
+//   linear_tile_kernel   one 128 x BN output tile per thread block (or per cluster of up
+//                        to 8 blocks that share the tile's reduction and add their
+//                        partial tiles through distributed shared memory in a fixed
+//                        order). With few rows the roles are exchanged: the 128 side runs
+//                        along the weight's columns and BN (16 to 128) along the rows.
+//
+// The sums, the bias, the activation and the residual are fp32; the one rounding is the
+// store to bf16.
+#include <cuda.h>
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+#include <cstdint>
+#include <cstring>
+
+#include "block_ops.h"
+#include "linear_epi.cuh"
+#include "sm100.cuh"
+#include "tma_map.h"
+
+namespace infini {
+namespace {
+
+constexpr int kKStep = 64;  // reduction elements per ring stage: one 128-byte swizzle row
+
+__device__ __forceinline__ void tma_load_tile(void* smem_dst, const CUtensorMap* m, uint64_t* bar,
+                                              int c0, int c1) {
+  asm volatile(
+      "cp.async.bulk.tensor.2d.shared::cta.global.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%3, %4}], [%2];" ::"r"(smem_u32(smem_dst)),
+      "l"(reinterpret_cast<uint64_t>(m)), "r"(smem_u32(bar)), "r"(c0), "r"(c1)
+      : "memory");
+}
+
+// A wait without the error report, for work that is in flight when a block leaves.
+__device__ __forceinline__ void drain_wait(uint64_t* bar, uint32_t parity) {
+  const uint32_t a = smem_u32(bar);
+  const uint64_t t0 = globaltimer_ns();
+  while (!mbar_try_wait(a, parity)) {
+    if (globaltimer_ns() - t0 > 200000000ull) break;  // 200 ms
+  }
+}
+
+// Operand tile of `mn` rows or columns x 64 reduction elements in shared memory: K-major,
+// mn rows of 128 bytes; MN-major, blocks of 64 columns, each 64 rows of 128 bytes (8 KB).
+// Descriptor of its kk-th 16 reduction elements:
+__device__ __forceinline__ uint64_t operand_desc(bool mn_major, uint32_t base, int kk) {
+  return mn_major ? sdesc(base + (uint32_t)kk * 2048, 8192, 1024)
+                  : sdesc(base + (uint32_t)kk * 32, 16, 1024);
+}
+
+struct Epilogue {
+  const float* bias;
+  const __nv_bfloat16* res;
+  __nv_bfloat16* out;
+  __nv_bfloat16* pre;
+  long long ldr, ldo, ldp;
+  int act;
+};
+
+__device__ __forceinline__ float4 ld_cluster_f4(uint32_t addr) {
+  float4 v;
+  asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+               : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+               : "r"(addr)
+               : "memory");
+  return v;
+}
+
+__device__ __forceinline__ float bf16_lo(uint32_t v) { return __uint_as_float(v << 16); }
+__device__ __forceinline__ float bf16_hi(uint32_t v) { return __uint_as_float(v & 0xffff0000u); }
+
+__device__ __forceinline__ uint4 pack8(const float (&v)[8]) {
+  return make_uint4(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]), pack_bf16x2(v[4], v[5]),
+                    pack_bf16x2(v[6], v[7]));
+}
+
+// Eight neighbouring outputs of one row (the row length is a multiple of 8, so that a
+// group of 8 is inside or outside as a whole).
+__device__ __forceinline__ void finish8(float (&v)[8], const Epilogue& e, long long row,
+                                        long long col) {
+  if (e.bias) {
+    const float4 b0 = __ldg(reinterpret_cast<const float4*>(e.bias + col));
+    const float4 b1 = __ldg(reinterpret_cast<const float4*>(e.bias + col + 4));
+    v[0] += b0.x; v[1] += b0.y; v[2] += b0.z; v[3] += b0.w;
+    v[4] += b1.x; v[5] += b1.y; v[6] += b1.z; v[7] += b1.w;
+  }
+  if (e.pre) *reinterpret_cast<uint4*>(e.pre + row * e.ldp + col) = pack8(v);
+  with_act(e.act, [&](auto a) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] = act_value<decltype(a)::value>(v[i]);
+  });
+  if (e.res) {
+    const uint4 r = *reinterpret_cast<const uint4*>(e.res + row * e.ldr + col);
+    const uint32_t w[4] = {r.x, r.y, r.z, r.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      v[2 * i] += bf16_lo(w[i]);
+      v[2 * i + 1] += bf16_hi(w[i]);
+    }
+  }
+  *reinterpret_cast<uint4*>(e.out + row * e.ldo + col) = pack8(v);
+}
+
+// ---- one tile per block or cluster ------------------------------------------------------
+
+struct TileParams {
+  unsigned tiles_b;  // BN-wide tiles along the B side
+  int ksteps;        // of the whole reduction
+  int split;         // blocks (cluster size) sharing the reduction
+  int a_mn, b_mn;
+  long long rows, cols;  // of the output
+  Epilogue epi;
+};
+
+constexpr int kTileThreads = 256;
+constexpr int tile_stages(int bn) { return bn <= 16 ? 10 : bn <= 32 ? 9 : bn <= 64 ? 8 : 6; }
+constexpr int tile_stage_bytes(int bn) { return (128 + bn) * 128; }
+constexpr int tile_smem(int bn) { return tile_stages(bn) * tile_stage_bytes(bn) + 256 + 1024; }
+// the fp32 tile that the ring's memory holds after the products: rows of (columns + 4)
+static_assert(128 * (128 + 4) * 4 <= tile_stages(128) * tile_stage_bytes(128), "tile fits");
+static_assert(128 * (64 + 4) * 4 <= tile_stages(64) * tile_stage_bytes(64), "tile fits");
+static_assert(32 * (128 + 4) * 4 <= tile_stages(32) * tile_stage_bytes(32), "tile fits");
+static_assert(16 * (128 + 4) * 4 <= tile_stages(16) * tile_stage_bytes(16), "tile fits");
+
+// Warps 0-3 drain the accumulator, warp 4 brings the operands (TMA), warp 5 issues the
+// products; all eight warps share the epilogue, which goes through shared memory: the
+// accumulator's lanes are output rows (or, with SWAP, output columns), and the pass
+// through an fp32 tile gives whole 16-byte pieces of output rows to neighbouring threads
+// in both cases, and a place from which the blocks of a cluster add their partial sums.
+// Bound by the stream of the weights with few rows: every block keeps its whole ring
+// (160 to 192 KB) in flight.
+template <int BN, bool SWAP>
+__global__ void __launch_bounds__(kTileThreads, 1)
+linear_tile_kernel(const __grid_constant__ CUtensorMap tm_a,
+                   const __grid_constant__ CUtensorMap tm_b, const TileParams p) {
+  constexpr int ST = tile_stages(BN);
+  constexpr int kABytes = 128 * 128, kStage = tile_stage_bytes(BN);
+  constexpr int kTileRows = SWAP ? BN : 128, kTileCols = SWAP ? 128 : BN;
+  constexpr int kLd = kTileCols + 4;  // floats; 4 of padding keep 16-byte row writes apart
+  constexpr uint32_t kTmemCols = BN < 32 ? 32 : BN;
+  extern __shared__ __align__(1024) uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
+                                             ~uintptr_t(1023));
+  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + ST * kStage);
+  uint64_t *full = bars, *empty = bars + ST, *acc = bars + 2 * ST;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(acc + 1);
+  float* tile = reinterpret_cast<float*>(smem);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const unsigned rank = p.split > 1 ? cluster_ctarank() : 0u;
+  const unsigned t = blockIdx.x / (unsigned)p.split;
+  const int a0 = 128 * (int)(t / p.tiles_b), b0 = BN * (int)(t % p.tiles_b);
+  const int ks0 = (int)((long long)p.ksteps * rank / p.split);
+  const int ks1 = (int)((long long)p.ksteps * (rank + 1) / p.split);
+
+  if (threadIdx.x == 0) {
+    for (int x = 0; x < 2 * ST + 1; ++x) mbar_init(&bars[x], 1);
+    fence_barrier_init();
+    tma_prefetch_desc(&tm_a);
+    tma_prefetch_desc(&tm_b);
+  }
+  if (warp == 5) {
+    tmem_alloc(tmem_slot, kTmemCols);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+
+  if (warp == 4) {
+    if (lane == 0) {
+      int issued = 0;
+      for (int ks = ks0; ks < ks1; ++ks, ++issued) {
+        const int st = issued % ST, use = issued / ST;
+        if (use > 0 && !mbar_wait(&empty[st], (uint32_t)((use - 1) & 1))) break;
+        uint8_t* sa = smem + st * kStage;
+        uint8_t* sb = sa + kABytes;
+        const int k = kKStep * ks;
+        mbar_arrive_expect_tx(&full[st], (uint32_t)kStage);
+        if (p.a_mn) {
+          tma_load_tile(sa, &tm_a, &full[st], a0, k);
+          tma_load_tile(sa + 8192, &tm_a, &full[st], a0 + 64, k);
+        } else {
+          tma_load_tile(sa, &tm_a, &full[st], k, a0);
+        }
+        if (BN >= 64 && p.b_mn) {
+#pragma unroll
+          for (int i = 0; i < (BN + 63) / 64; ++i)
+            tma_load_tile(sb + 8192 * i, &tm_b, &full[st], b0 + 64 * i, k);
+        } else {
+          tma_load_tile(sb, &tm_b, &full[st], k, b0);
+        }
+      }
+      // every copy into this block's ring has landed before the ring is reused or left
+      for (int st = 0; st < ST && st < issued; ++st)
+        drain_wait(&full[st], (uint32_t)(((issued - 1 - st) / ST) & 1));
+    }
+    __syncwarp();
+  } else if (warp == 5) {
+    const uint32_t idesc = idesc_f32acc(1, (uint32_t)p.a_mn, (uint32_t)p.b_mn, 128, BN);
+    for (int ks = ks0, it = 0; ks < ks1; ++ks, ++it) {
+      const int st = it % ST;
+      if (!mbar_wait_warp(&full[st], (uint32_t)((it / ST) & 1))) break;
+      tc_fence_after();
+      if (elect_one()) {
+        const uint32_t sa = smem_u32(smem + st * kStage), sb = sa + kABytes;
+#pragma unroll
+        for (int kk = 0; kk < kKStep / 16; ++kk)
+          mma_bf16_ss(tmem, operand_desc(p.a_mn, sa, kk), operand_desc(p.b_mn, sb, kk), idesc,
+                      (it > 0 || kk > 0) ? 1u : 0u);
+        mma_commit(&empty[st]);
+      }
+      __syncwarp();
+    }
+    if (elect_one()) mma_commit(acc);  // all products done: sums complete, ring free
+    __syncwarp();
+  }
+  // the products are done (for every warp: the ring's memory becomes the fp32 tile)
+  mbar_wait_warp(acc, 0);
+  __syncthreads();
+  if (warp < 4) {
+    tc_fence_after();
+    const int m = warp * 32 + lane;  // index along the 128 side
+#pragma unroll
+    for (int c = 0; c < BN; c += 32) {
+      uint32_t v[32];
+      tmem_ld32(tmem + ((uint32_t)(warp * 32) << 16) + (uint32_t)c, v);
+      tmem_wait_ld();
+      if (SWAP) {
+#pragma unroll
+        for (int i = 0; i < 32; ++i)
+          if (c + i < BN) tile[(c + i) * kLd + m] = __uint_as_float(v[i]);
+      } else {
+#pragma unroll
+        for (int i = 0; i < 32; i += 4)
+          *reinterpret_cast<uint4*>(&tile[m * kLd + c + i]) =
+              make_uint4(v[i], v[i + 1], v[i + 2], v[i + 3]);
+      }
+    }
+    tc_fence_before();
+  }
+  if (p.split > 1)
+    cluster_sync_all();
+  else
+    __syncthreads();
+  if (warp == 5) {
+    tc_fence_after();
+    tmem_dealloc(tmem, kTmemCols);
+  }
+
+  // Epilogue: this block's share of the tile's 16-byte output pieces.
+  constexpr int kPerRow = kTileCols / 8;
+  constexpr unsigned kUnits = kTileRows * kPerRow;
+  const unsigned u0 = kUnits * rank / (unsigned)p.split;
+  const unsigned u1 = kUnits * (rank + 1) / (unsigned)p.split;
+  const long long row0 = SWAP ? b0 : a0, col0 = SWAP ? a0 : b0;
+  for (unsigned u = u0 + threadIdx.x; u < u1; u += kTileThreads) {
+    const int r = (int)(u / kPerRow), c = 8 * (int)(u % kPerRow);
+    if (row0 + r >= p.rows || col0 + c >= p.cols) continue;
+    const float* src = &tile[r * kLd + c];
+    float v[8];
+    if (p.split > 1) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) v[i] = 0.f;
+      for (int q = 0; q < p.split; ++q) {  // in rank order: the same sums every time
+        const uint32_t a = smem_cluster_addr(src, (uint32_t)q);
+        const float4 x = ld_cluster_f4(a), y = ld_cluster_f4(a + 16);
+        v[0] += x.x; v[1] += x.y; v[2] += x.z; v[3] += x.w;
+        v[4] += y.x; v[5] += y.y; v[6] += y.z; v[7] += y.w;
+      }
+    } else {
+      const float4 x = *reinterpret_cast<const float4*>(src);
+      const float4 y = *reinterpret_cast<const float4*>(src + 4);
+      v[0] = x.x; v[1] = x.y; v[2] = x.z; v[3] = x.w;
+      v[4] = y.x; v[5] = y.y; v[6] = y.z; v[7] = y.w;
+    }
+    finish8(v, p.epi, row0 + r, col0 + c);
+  }
+  // no block of the cluster leaves while another reads its tile
+  if (p.split > 1) {
+    __syncwarp();
+    cluster_sync_all();
+  }
+}
+
+// ---- host side --------------------------------------------------------------------------
+
+// Map over a stored matrix [outer][inner], rows ld elements apart; boxes of 64 inner x
+// box_outer outer elements, 128-byte swizzle. Reads outside the matrix give zeros.
+bool make_map(CUtensorMap* m, const void* base, long long inner, long long outer, long long ld,
+              uint32_t box_outer) {
+  EncodeTiledFn enc = get_encode_fn();
+  if (!enc) return false;
+  const cuuint64_t dims[2] = {(cuuint64_t)inner, (cuuint64_t)outer};
+  const cuuint64_t strides[1] = {(cuuint64_t)ld * 2};
+  const cuuint32_t box[2] = {64, box_outer};
+  const cuuint32_t estr[2] = {1, 1};
+  return enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(base), dims, strides, box,
+             estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// Map of an operand whose tile is `mn` rows or columns wide.
+bool operand_map(CUtensorMap* m, const __nv_bfloat16* p, long long ld, bool mn_major,
+                 long long extent, long long R, int mn) {
+  return mn_major ? make_map(m, p, extent, R, ld, 64) : make_map(m, p, R, extent, ld, (uint32_t)mn);
+}
+
+template <int BN, bool SWAP>
+cudaError_t tile_launch(const GemmArgs& g, int split, cudaStream_t stream) {
+  const long long a_extent = SWAP ? g.Q : g.P, b_extent = SWAP ? g.P : g.Q;
+  CUtensorMap ma, mb;
+  const bool ok = SWAP ? operand_map(&ma, g.b, g.ldb, g.b_mn, g.Q, g.R, 128) &&
+                             operand_map(&mb, g.a, g.lda, g.a_mn, g.P, g.R, BN)
+                       : operand_map(&ma, g.a, g.lda, g.a_mn, g.P, g.R, 128) &&
+                             operand_map(&mb, g.b, g.ldb, g.b_mn, g.Q, g.R, BN);
+  if (!ok) return cudaErrorInvalidValue;
+  TileParams p;
+  const long long tiles_b = (b_extent + BN - 1) / BN;
+  const long long blocks = (a_extent + 127) / 128 * tiles_b * split;
+  if (blocks >= (1ll << 31)) return cudaErrorInvalidValue;
+  p.tiles_b = (unsigned)tiles_b;
+  p.ksteps = (int)((g.R + kKStep - 1) / kKStep);
+  p.split = split;
+  p.a_mn = SWAP ? g.b_mn : g.a_mn;
+  p.b_mn = SWAP ? g.a_mn : g.b_mn;
+  p.rows = g.P;
+  p.cols = g.Q;
+  p.epi = Epilogue{g.bias, g.res, g.out, g.pre, g.ldr, g.ldo, g.ldp, g.act};
+  cudaLaunchConfig_t cfg;
+  memset(&cfg, 0, sizeof(cfg));
+  cfg.gridDim = dim3((unsigned)blocks);
+  cfg.blockDim = dim3(kTileThreads);
+  cfg.dynamicSmemBytes = tile_smem(BN);
+  cfg.stream = stream;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeClusterDimension;
+  at[0].val.clusterDim.x = (unsigned)split;
+  at[0].val.clusterDim.y = 1;
+  at[0].val.clusterDim.z = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = split > 1 ? 1 : 0;
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, linear_tile_kernel<BN, SWAP>, ma, mb, p);
+  return e != cudaSuccess ? e : cudaGetLastError();
+}
+
+// Blocks that share one tile's reduction: as many (a power of two, 8 at most) as one wave
+// of blocks has room for, each with two k-steps at least.
+int tile_split(long long tiles, long long ksteps, int sms) {
+  int s = 1;
+  while (s < 8 && tiles * 2 * s <= sms && ksteps >= 4 * s) s *= 2;
+  return s;
+}
+
+template <typename K>
+cudaError_t set_smem(K* kernel, int bytes) {
+  return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+}
+
+}  // namespace
+
+cudaError_t linear_set_attributes() {
+  cudaError_t e = set_smem(linear_tile_kernel<16, true>, tile_smem(16));
+  if (e == cudaSuccess) e = set_smem(linear_tile_kernel<32, true>, tile_smem(32));
+  if (e == cudaSuccess) e = set_smem(linear_tile_kernel<64, true>, tile_smem(64));
+  if (e == cudaSuccess) e = set_smem(linear_tile_kernel<128, false>, tile_smem(128));
+  return e;
+}
+
+size_t linear_gemm_scratch(long long, long long, long long, bool, int) { return 0; }
+
+cudaError_t linear_gemm_launch(const GemmArgs& g, void*, int sms, cudaStream_t stream) {
+  const long long ksteps = (g.R + kKStep - 1) / kKStep;
+  // Few rows, stored along the reduction: the rows take the narrow side of the tile.
+  if (g.P <= 64 && !g.a_mn) {
+    const int s = tile_split((g.Q + 127) / 128, ksteps, sms);
+    if (g.P <= 16) return tile_launch<16, true>(g, s, stream);
+    if (g.P <= 32) return tile_launch<32, true>(g, s, stream);
+    return tile_launch<64, true>(g, s, stream);
+  }
+  const long long tiles = (g.P + 127) / 128 * ((g.Q + 127) / 128);
+  return tile_launch<128, false>(g, tile_split(tiles, ksteps, sms), stream);
+}
+
+// ---- the activation's gradient and the bias gradient --------------------------------------
+
+namespace {
+
+constexpr int kActCols = 256;  // columns of a block: 32 lanes x 8
+constexpr int kActWarps = 8;
+
+// dpre = dy act'(pre), one 16-byte piece of a row per thread and step, and the column
+// sums of dpre before its rounding (fp32, one row of `part` per row chunk). HBM-bound:
+// dy and pre read once, dpre written once.
+template <int ACT>
+__global__ void __launch_bounds__(32 * kActWarps)
+act_grad_kernel(const __nv_bfloat16* __restrict__ dy, long long lddy,
+                const __nv_bfloat16* __restrict__ pre, long long ldp,
+                __nv_bfloat16* __restrict__ dpre, float* __restrict__ part, long long M, int N) {
+  __shared__ float sums[kActWarps][kActCols];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int col = blockIdx.x * kActCols + 8 * lane;
+  const bool in = col < N;
+  const long long r0 = M * blockIdx.y / gridDim.y, r1 = M * (blockIdx.y + 1) / gridDim.y;
+  float s[8] = {};
+  if (in) {
+#pragma unroll 4
+    for (long long r = r0 + warp; r < r1; r += kActWarps) {
+      const uint4 g = __ldg(reinterpret_cast<const uint4*>(dy + r * lddy + col));
+      const uint32_t gw[4] = {g.x, g.y, g.z, g.w};
+      float d[8];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        d[2 * i] = bf16_lo(gw[i]);
+        d[2 * i + 1] = bf16_hi(gw[i]);
+      }
+      if (ACT != kActNone) {
+        const uint4 z = __ldg(reinterpret_cast<const uint4*>(pre + r * ldp + col));
+        const uint32_t zw[4] = {z.x, z.y, z.z, z.w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          d[2 * i] *= act_deriv<ACT>(bf16_lo(zw[i]));
+          d[2 * i + 1] *= act_deriv<ACT>(bf16_hi(zw[i]));
+        }
+        // bf16 because the tensor cores read it: 2^-9 relative, as every operand's rounding
+        *reinterpret_cast<uint4*>(dpre + r * (long long)N + col) = pack8(d);
+      }
+#pragma unroll
+      for (int i = 0; i < 8; ++i) s[i] += d[i];
+    }
+  }
+  if (!part) return;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) sums[warp][8 * lane + i] = s[i];
+  __syncthreads();
+  const int c = blockIdx.x * kActCols + threadIdx.x;
+  if (c < N) {
+    float v = 0.f;
+#pragma unroll
+    for (int w = 0; w < kActWarps; ++w) v += sums[w][threadIdx.x];
+    part[(long long)blockIdx.y * N + c] = v;
+  }
+}
+
+// Fixed-order column sums: 32 columns x 8 partial sums of every eighth row.
+__global__ void __launch_bounds__(256) colsum_kernel(const ColsumArgs a) {
+  __shared__ float sums[8][33];
+  const int lane = threadIdx.x & 31, w = threadIdx.x >> 5, set = blockIdx.y;
+  if (!a.out[set]) return;
+  const int c = blockIdx.x * 32 + lane;
+  float v = 0.f;
+  if (c < a.D)
+#pragma unroll 4
+    for (long long k = w; k < a.count; k += 8) v += a.part[(k * a.sets + set) * a.D + c];
+  sums[w][lane] = v;
+  __syncthreads();
+  if (w == 0 && c < a.D) {
+#pragma unroll
+    for (int i = 1; i < 8; ++i) v += sums[i][lane];
+    a.out[set][c] = v;
+  }
+}
+
+}  // namespace
+
+int act_grad_chunks(long long M, int N, int sms) {
+  // about eight blocks per SM, 8 rows per warp at least
+  const long long across = (N + kActCols - 1) / kActCols;
+  long long c = (8ll * sms + across - 1) / across;
+  const long long most = (M + 8 * kActWarps - 1) / (8 * kActWarps);
+  c = c < most ? c : most;
+  return (int)(c < 1 ? 1 : (c > 65535 ? 65535 : c));
+}
+
+cudaError_t act_grad_launch(const __nv_bfloat16* dy, long long lddy, const __nv_bfloat16* pre,
+                            long long ldp, int act, __nv_bfloat16* dpre, float* part, int chunks,
+                            long long M, int N, cudaStream_t stream) {
+  const dim3 grid((unsigned)((N + kActCols - 1) / kActCols), (unsigned)chunks);
+  switch (act) {
+#define INFINI_ACT_CASE(A)                                                                     \
+  case A:                                                                                      \
+    act_grad_kernel<A><<<grid, 32 * kActWarps, 0, stream>>>(dy, lddy, pre, ldp, dpre, part, M, \
+                                                            N);                                \
+    break;
+    INFINI_ACT_CASE(kActNone)
+    INFINI_ACT_CASE(kActRelu)
+    INFINI_ACT_CASE(kActSilu)
+    INFINI_ACT_CASE(kActGelu)
+    INFINI_ACT_CASE(kActGeluTanh)
+#undef INFINI_ACT_CASE
+    default: return cudaErrorInvalidValue;
+  }
+  return cudaGetLastError();
+}
+
+cudaError_t colsum_launch(const ColsumArgs& a, cudaStream_t stream) {
+  colsum_kernel<<<dim3((unsigned)((a.D + 31) / 32), (unsigned)a.sets), 256, 0, stream>>>(a);
+  return cudaGetLastError();
+}
+
+}  // namespace infini

@@ -1,0 +1,128 @@
+// norm_fwd.cu — the norms around a block, with the block's gate and the scaled residual
+// stream, in one pass over the rows:
+//
+//   u = post(b)            (or b)             post, pre: n(v) w + c with
+//   r = alpha x + gate u   (or alpha x + u)   n(v) = v / sqrt(mean v^2 + eps), or
+//   h = pre(r)                                n(v) = (v - mean v) / sqrt(var v + eps)
+//
+// b absent: r = alpha x, so that h is the plain norm of x. Everything between the loads
+// and the two stores is fp32 in registers; h is formed from the unrounded r.
+// HBM-bound: x and b read once, r and h written once. A worker (threads of one row) asks
+// for its next row before it works on the present one.
+#include "norm_common.cuh"
+
+namespace infini {
+namespace {
+
+template <typename T, int TPR, bool VEC, bool LAYER>
+__global__ void __launch_bounds__(norm_threads(TPR))
+norm_forward_kernel(const NormArgs a) {
+  using L = RowLayout<T, TPR, VEC>;
+  constexpr int kWorkers = norm_threads(TPR) / TPR;
+  __shared__ float2 sbuf[kWorkers][2][TPR / 32];
+  const int w = threadIdx.x / TPR, t = threadIdx.x % TPR;
+  RowSum<TPR> red{&sbuf[w], 1 + w};
+  const float inv_d = 1.f / (float)a.D;
+  const int D = a.D;
+  const long long step = (long long)gridDim.x * kWorkers;
+  long long row = (long long)blockIdx.x * kWorkers + w;
+  RowRaw<T, TPR, VEC> nx, nb;
+  if (row < a.rows) {
+    nx.load(a.x, row, D, t);
+    if (a.b) nb.load(a.b, row, D, t);
+  }
+  for (; row < a.rows; row += step) {
+    float v[kE], q[kE];
+    nx.get(v);
+#pragma unroll
+    for (int i = 0; i < kE; ++i) v[i] *= a.alpha;
+    if (a.b) {
+      float u[kE];
+      nb.get(u);
+      if (row + step < a.rows) {
+        nx.load(a.x, row + step, D, t);
+        nb.load(a.b, row + step, D, t);
+      }
+      if (a.post_w) {
+        normalise<L, LAYER>(u, t, D, inv_d, a.eps, red);
+        load_param<L, VEC>(a.post_w, D, t, q);
+#pragma unroll
+        for (int i = 0; i < kE; ++i) u[i] *= q[i];
+        if (a.post_b) {
+          load_param<L, VEC>(a.post_b, D, t, q);
+#pragma unroll
+          for (int i = 0; i < kE; ++i) u[i] += q[i];
+        }
+      }
+      if (a.gate) {
+        load_param<L, VEC>(a.gate + (row / a.group_rows) * D, D, t, q);
+#pragma unroll
+        for (int i = 0; i < kE; ++i) u[i] *= q[i];
+      }
+#pragma unroll
+      for (int i = 0; i < kE; ++i) v[i] += u[i];
+    } else if (row + step < a.rows) {
+      nx.load(a.x, row + step, D, t);
+    }
+    if (a.r) store_row<T, TPR, VEC>(a.r, row, D, t, v);
+    if (a.h) {
+      normalise<L, LAYER>(v, t, D, inv_d, a.eps, red);
+      load_param<L, VEC>(a.pre_w, D, t, q);
+#pragma unroll
+      for (int i = 0; i < kE; ++i) v[i] *= q[i];
+      if (a.pre_b) {
+        load_param<L, VEC>(a.pre_b, D, t, q);
+#pragma unroll
+        for (int i = 0; i < kE; ++i) v[i] += q[i];
+      }
+      store_row<T, TPR, VEC>(a.h, row, D, t, v);
+    }
+  }
+}
+
+template <typename T, int TPR, bool VEC>
+cudaError_t launch(const NormArgs& a, int kind, int sms, cudaStream_t stream) {
+  constexpr int kThreads = norm_threads(TPR), kWorkers = kThreads / TPR;
+  const long long need = (a.rows + kWorkers - 1) / kWorkers;
+  const long long most = (long long)sms * (2048 / kThreads);
+  const unsigned grid = (unsigned)(need < most ? need : most);
+  if (kind == kNormLayer)
+    norm_forward_kernel<T, TPR, VEC, true><<<grid, kThreads, 0, stream>>>(a);
+  else
+    norm_forward_kernel<T, TPR, VEC, false><<<grid, kThreads, 0, stream>>>(a);
+  return cudaGetLastError();
+}
+
+template <typename T, bool VEC>
+cudaError_t by_width(const NormArgs& a, int kind, int sms, cudaStream_t stream) {
+  switch (norm_tpr(a.D)) {
+    case 32: return launch<T, 32, VEC>(a, kind, sms, stream);
+    case 128: return launch<T, 128, VEC>(a, kind, sms, stream);
+    case 256: return launch<T, 256, VEC>(a, kind, sms, stream);
+    case 512: return launch<T, 512, VEC>(a, kind, sms, stream);
+    default: return launch<T, 1024, VEC>(a, kind, sms, stream);
+  }
+}
+
+bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+
+}  // namespace
+
+// Every row of every array starts on 16 bytes.
+bool norm_vectorised(const NormArgs& a, bool f32) {
+  return a.D % (f32 ? 4 : 8) == 0 && aligned16(a.x) && aligned16(a.b) && aligned16(a.r) &&
+         aligned16(a.h) && aligned16(a.dr) && aligned16(a.dh) && aligned16(a.dx) &&
+         aligned16(a.db) && aligned16(a.gate) && aligned16(a.post_w) && aligned16(a.post_b) &&
+         aligned16(a.pre_w) && aligned16(a.pre_b);
+}
+
+cudaError_t norm_forward_launch(const NormArgs& a, int kind, bool f32, int sms,
+                                cudaStream_t stream) {
+  if (norm_vectorised(a, f32))
+    return f32 ? by_width<float, true>(a, kind, sms, stream)
+               : by_width<__nv_bfloat16, true>(a, kind, sms, stream);
+  return f32 ? by_width<float, false>(a, kind, sms, stream)
+             : by_width<__nv_bfloat16, false>(a, kind, sms, stream);
+}
+
+}  // namespace infini

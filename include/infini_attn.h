@@ -347,6 +347,205 @@ int infini_attn_backward_ex(const void* q, const void* k, const void* v, const f
 size_t infini_attn_backward_workspace_size(int B, int H, long long L, int N, int d, int mode);
 
 /*
+ * ---- The operators around the attention layer ----------------------------------------
+ *
+ * A transformer block puts the attention layer between norms, a gate and the residual
+ * stream, and follows it with an MLP: infini_attn_norm and infini_attn_residual_norm are
+ * the norms (with the gate and the scaled residual in the same pass), infini_attn_linear
+ * the MLP's products (with bias, activation and residual in the epilogue), each with its
+ * gradient; infini_attn_block_forward runs the whole block. All are asynchronous on
+ * `stream`, check their arguments on the host before any launch and keep no pointer. The
+ * device of the pointers and of the stream has to be the current one. Parameters come in
+ * structs; set the unused fields to 0 (NULL).
+ */
+
+/* Activations. */
+typedef enum {
+  INFINI_ACT_NONE = 0,
+  INFINI_ACT_RELU = 1,     /* max(v, 0), derivative 0 at 0 */
+  INFINI_ACT_SILU = 2,     /* v / (1 + e^-v) */
+  INFINI_ACT_GELU = 3,     /* v (1 + erf(v / sqrt 2)) / 2 */
+  INFINI_ACT_GELU_TANH = 4 /* v (1 + tanh(sqrt(2 / pi) (v + 0.044715 v^3))) / 2 */
+} infini_act_t;
+
+/*
+ * y = act(x W + bias) + residual
+ *   x         bf16 [M][K]; W bf16 [K][N]; y bf16 [M][N], written
+ *   bias      fp32 [N] or NULL
+ *   residual  bf16 [M][N] or NULL; may be y itself (same pointer and row stride)
+ *   preact    bf16 [M][N] or NULL: x W + bias is written here (what the gradient of an
+ *             activation needs)
+ *   ld*       row strides in elements, multiples of 8, at least the row length; 0 means
+ *             contiguous rows
+ * Products are summed in fp32; bias, activation and residual are applied in fp32 and y
+ * (and preact) rounded once. M >= 0 (0: nothing to do), K and N multiples of 8
+ * (INFINI_ERR_UNSUPPORTED otherwise), M < 2^31; every pointer 16-byte aligned; y and preact
+ * may not overlap each other or an input (but for residual == y). No scratch. The result
+ * depends on the sizes and the device only (fixed order of every sum).
+ */
+typedef struct {
+  const void* x;
+  const void* W;
+  const float* bias;
+  const void* residual;
+  void* y;
+  void* preact;
+  long long ldx, ldw, ldr, ldy, ldp;
+  long long M;
+  int K, N, act;
+} infini_attn_linear_t;
+
+int infini_attn_linear(const infini_attn_linear_t* p, void* stream);
+
+/*
+ * Gradient of infini_attn_linear for the loss sum(dy * y): with d = dy * act'(preact),
+ *   dx = d W^T (bf16 [M][K]),  dW = x^T d (bf16 [K][N]),  dbias = sum of d's rows (fp32 [N]).
+ * Each may be NULL; W is needed for dx, x for dW, preact unless act is NONE. The residual's
+ * gradient is dy. d is rounded to bf16 as an operand of the two products; dbias sums the
+ * unrounded d in fp32. M = 0 writes zeros to dW and dbias. Sizes, strides and alignment as
+ * for infini_attn_linear. No output may overlap an input or another output. Scratch:
+ * infini_attn_linear_backward_workspace_size bytes from opts->workspace (256-byte aligned)
+ * or the stream-ordered allocator; opts may be NULL. opts->stage_events[0..2] are recorded
+ * at the start, after d and dbias, and at the end. Bitwise reproducible.
+ */
+typedef struct {
+  const void* x;
+  const void* W;
+  const void* preact;
+  const void* dy;
+  void* dx;
+  void* dW;
+  float* dbias;
+  long long ldx, ldw, ldp, lddy, lddx, lddw;
+  long long M;
+  int K, N, act;
+} infini_attn_linear_grad_t;
+
+int infini_attn_linear_backward(const infini_attn_linear_grad_t* p,
+                                const infini_attn_opts_t* opts, void* stream);
+
+/* Scratch bytes of infini_attn_linear_backward with all three outputs (0 when M is 0 or the
+ * sizes are not supported). */
+size_t infini_attn_linear_backward_workspace_size(long long M, int K, int N, int act);
+
+/* Norms over a row v of `dim` values: n(v) = v / sqrt(mean v^2 + eps) or
+ * (v - mean v) / sqrt(var v + eps), then n(v) * weight + bias. */
+typedef enum { INFINI_NORM_RMS = 0, INFINI_NORM_LAYER = 1 } infini_norm_t;
+
+/*
+ * The norms after a block and before the next one, the block's gate and the scaled
+ * residual stream in one pass over the rows:
+ *   u = norm(b; post_weight, post_bias)   (u = b without post_weight)
+ *   r = alpha x + gate u                  (r = alpha x without b)
+ *   h = norm(r; pre_weight, pre_bias)     (from the unrounded r)
+ *   x, b, r, h   [rows][dim], all bf16 or all fp32 (dtype), contiguous. b may be NULL. r or h
+ *                may be NULL (not written); each may be x or b itself, but no other overlap.
+ *   gate         fp32 [gate_groups][dim] or NULL; row i takes gate row
+ *                i / (rows / gate_groups): 1 group gates all rows alike, one per batch entry
+ *                gates each sequence, `rows` groups gate each token
+ *   post_*, pre_*  fp32 [dim]; a norm is there when its weight is, its bias (layer norm
+ *                only) may be NULL
+ * rows >= 0; 1 <= dim <= 8192 (INFINI_ERR_UNSUPPORTED beyond); eps >= 0. No alignment beyond
+ * the types' own is needed; rows that all start on 16 bytes are read faster. No scratch.
+ */
+typedef struct {
+  const void* x;
+  const void* b;
+  const float* gate;
+  const float* post_weight;
+  const float* post_bias;
+  const float* pre_weight;
+  const float* pre_bias;
+  void* r;
+  void* h;
+  long long rows, gate_groups;
+  int dim, kind, dtype;
+  float alpha, eps;
+} infini_attn_residual_norm_t;
+
+int infini_attn_residual_norm(const infini_attn_residual_norm_t* p, void* stream);
+
+/*
+ * Gradient of infini_attn_residual_norm for the loss sum(dr * r) + sum(dh * h). p gives the
+ * forward's inputs (its r and h are not used). dr or dh may be NULL (zero). dx, db: like x and
+ * b (each may be one of x, b, dr, dh itself); dgate: like gate, summed over each group's
+ * rows; the others [dim], summed over all rows; all sums fp32, any output may be NULL.
+ * rows = 0 writes zeros to the sums. Scratch
+ * (infini_attn_residual_norm_backward_workspace_size) from opts->workspace (256-byte
+ * aligned) or the stream-ordered allocator; opts may be NULL. Bitwise reproducible.
+ */
+typedef struct {
+  const void* dr;
+  const void* dh;
+  void* dx;
+  void* db;
+  float* dgate;
+  float* dpost_weight;
+  float* dpost_bias;
+  float* dpre_weight;
+  float* dpre_bias;
+} infini_attn_residual_norm_grad_t;
+
+int infini_attn_residual_norm_backward(const infini_attn_residual_norm_t* p,
+                                       const infini_attn_residual_norm_grad_t* g,
+                                       const infini_attn_opts_t* opts, void* stream);
+
+/* Scratch bytes of the gradient with every output (gate_groups 0: no gate). */
+size_t infini_attn_residual_norm_backward_workspace_size(long long rows, int dim,
+                                                         long long gate_groups, int kind);
+
+/* h = norm(x; weight, bias): infini_attn_residual_norm without a block's output; and its
+ * gradient (dx, dweight, dbias; each may be NULL, dbias for a layer norm only), with the
+ * scratch of infini_attn_residual_norm_backward_workspace_size(rows, dim, 0, kind). */
+int infini_attn_norm(const void* x, const float* weight, const float* bias, void* h,
+                     long long rows, int dim, int kind, int dtype, float eps, void* stream);
+int infini_attn_norm_backward(const void* x, const float* weight, const void* dh, void* dx,
+                              float* dweight, float* dbias, long long rows, int dim, int kind,
+                              int dtype, float eps, const infini_attn_opts_t* opts, void* stream);
+
+/*
+ * One transformer block around the attention layer (bf16):
+ *   a = layer(norm(x; attn_norm))                  infini_attn_layer_forward
+ *   r = alpha x + attn_gate norm(a; attn_post_norm)
+ *   f = act(norm(r; mlp_norm) W_up + b_up) W_down + b_down
+ *   y = alpha r + mlp_gate norm(f; mlp_post_norm)
+ * x, y [B, L, D_model]; the layer's weights, beta, state, sizes and mode as for
+ * infini_attn_layer_forward, with its limits (d = 128, D_model and B * L multiples of 128)
+ * and D_model <= 8192; W_up [D_model][D_ff], W_down [D_ff][D_model] bf16, D_ff a multiple of
+ * 8; b_up [D_ff], b_down [D_model] fp32 or NULL; gates fp32 [gate_groups][D_model] or NULL
+ * (rows as for infini_attn_residual_norm; the same number of groups for both); post norms
+ * only where their weight is given. kind and eps apply to all four norms. Between the steps
+ * activations are rounded to bf16. y may not overlap anything that is read. Scratch
+ * (infini_attn_block_workspace_size bytes, 0 when the sizes are not supported) from
+ * opts->workspace (256-byte aligned) or the stream-ordered allocator; opts may be NULL.
+ * opts->stage_events[0..2] are recorded after the attention layer, after the norm that
+ * follows it, and at the end.
+ */
+typedef struct {
+  const void* x;
+  const void *Wq, *Wk, *Wv, *Wo;
+  const float* beta;
+  const float *M_in, *z_in;
+  float *M_out, *z_out;
+  const float *attn_norm, *attn_norm_bias, *attn_post_norm, *attn_post_norm_bias, *attn_gate;
+  const float *mlp_norm, *mlp_norm_bias, *mlp_post_norm, *mlp_post_norm_bias, *mlp_gate;
+  const void* W_up;
+  const float* b_up;
+  const void* W_down;
+  const float* b_down;
+  void* y;
+  long long L, gate_groups;
+  int B, D_model, D_ff, H, H_kv, N, d, mode, act, kind;
+  float alpha, eps;
+} infini_attn_block_t;
+
+int infini_attn_block_forward(const infini_attn_block_t* p, const infini_attn_opts_t* opts,
+                              void* stream);
+
+size_t infini_attn_block_workspace_size(int B, long long L, int D_model, int D_ff, int H,
+                                        int H_kv, int N, int d, int mode);
+
+/*
  * Device-side status of earlier calls on the current device: INFINI_OK, or
  * INFINI_ERR_TIMEOUT when a bounded wait inside a kernel ran out (the kernel
  * then stopped early and its outputs are invalid). Synchronises the device,
