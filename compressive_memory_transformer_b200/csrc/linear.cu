@@ -10,12 +10,18 @@
 //                        partial tiles through distributed shared memory in a fixed
 //                        order). With few rows the roles are exchanged: the 128 side runs
 //                        along the weight's columns and BN (16 to 128) along the rows.
+//   linear_pair_kernel   for large products: 256 x 256 tiles on pairs of SMs
+//                        (cta_group::2), persistent, two accumulators, so that the
+//                        epilogue of one tile runs beside the products of the next; with
+//                        few tiles the reduction is split over pairs as well, the partial
+//                        sums going through fp32 scratch to split_reduce_kernel.
 //
 // The sums, the bias, the activation and the residual are fp32; the one rounding is the
 // store to bf16.
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
+#include <atomic>
 #include <cstdint>
 #include <cstring>
 
@@ -290,6 +296,365 @@ linear_tile_kernel(const __grid_constant__ CUtensorMap tm_a,
   }
 }
 
+// ---- 256 x 256 tiles on pairs of SMs -----------------------------------------------------
+
+struct PairParams {
+  unsigned tiles_n, tiles;  // of 256 columns; in all
+  unsigned units;           // tiles * split
+  int ksteps, split;
+  int a_mn, b_mn;
+  long long rows, cols;
+  Epilogue epi;    // out, res and pre go through tensor maps
+  float* partial;  // split > 1: [split][rows][cols]
+};
+
+struct PairMaps {
+  CUtensorMap out, res, pre;  // boxes of 32 columns x 32 rows, 64-byte swizzle
+};
+
+constexpr int kPairThreads = 320;
+constexpr int kPairStages = 5;
+constexpr int kPairA = 16384, kPairStage = 2 * kPairA;  // this CTA's half of A and of B
+constexpr int kSlot = 2048;                             // 32 rows x 64 bytes
+constexpr int kPairStaging = 8 * 4 * kSlot;
+enum {
+  Q_FULL = 0,
+  Q_EMPTY = Q_FULL + kPairStages,
+  Q_AFULL = Q_EMPTY + kPairStages,
+  Q_AEMPTY = Q_AFULL + 2,
+  Q_DRAIN = Q_AEMPTY + 2,
+  Q_RES = Q_DRAIN + 1,  // two per epilogue warp
+  Q_COUNT = Q_RES + 16
+};
+static_assert(Q_COUNT * 8 + 4 <= 256, "barrier area");
+constexpr int kPairSmem = kPairStages * kPairStage + kPairStaging + 256 + 1024;
+
+// A copy into this CTA's shared memory that completes on a barrier of the pair (address in
+// the cluster's window).
+__device__ __forceinline__ void tma_load_half(void* smem_dst, const CUtensorMap* m,
+                                              uint32_t bar_cluster, int c0, int c1) {
+  asm volatile(
+      "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%3, %4}], [%2];" ::"r"(smem_u32(smem_dst)),
+      "l"(reinterpret_cast<uint64_t>(m)), "r"(bar_cluster), "r"(c0), "r"(c1)
+      : "memory");
+}
+
+__device__ __forceinline__ void tma_store_box(const CUtensorMap* m, const void* smem_src, int c0,
+                                              int c1) {
+  asm volatile(
+      "cp.async.bulk.tensor.2d.global.shared::cta.bulk_group [%0, {%2, %3}], [%1];" ::"l"(
+          reinterpret_cast<uint64_t>(m)),
+      "r"(smem_u32(smem_src)), "r"(c0), "r"(c1)
+      : "memory");
+}
+
+// Until at most one of this thread's bulk store groups still reads shared memory.
+__device__ __forceinline__ void bulk_wait_read_but_one() {
+  asm volatile("cp.async.bulk.wait_group.read 1;" ::: "memory");
+}
+
+__device__ __forceinline__ uint4 ld_shared_v4(uint32_t addr) {
+  uint4 v;
+  asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+               : "r"(addr)
+               : "memory");
+  return v;
+}
+
+// Place of 16-byte unit u (0..3) of row r in a box with the 64-byte swizzle.
+__device__ __forceinline__ uint32_t sw64(uint32_t r, uint32_t u) {
+  return r * 64u + ((u ^ ((r >> 1) & 3u)) << 4);
+}
+
+// Warps 0-7 of each CTA: epilogue (warp w drains accumulator lanes 32 (w % 4).. and columns
+// 128 (w / 4)..); warp 8: copies; warp 9 of the even CTA: the pair's products (M = 256,
+// N = 256, K = 16 each). Each k-step of 64 brings 128 rows (columns) of A and of B into
+// each CTA, both CTAs' copies completing on the even CTA's barrier. The epilogue takes 32
+// columns at a time: accumulator -> registers -> swizzled staging slot -> TMA store, which
+// writes whole sectors and clips at the edges; a residual comes into the same slot by a
+// TMA load one step ahead and is replaced by the output in place.
+__global__ void __launch_bounds__(kPairThreads, 1)
+linear_pair_kernel(const __grid_constant__ CUtensorMap tm_a,
+                   const __grid_constant__ CUtensorMap tm_b,
+                   const __grid_constant__ PairMaps io, const PairParams p) {
+  extern __shared__ __align__(1024) uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
+                                             ~uintptr_t(1023));
+  uint8_t* staging = smem + kPairStages * kPairStage;
+  uint64_t* bars = reinterpret_cast<uint64_t*>(staging + kPairStaging);
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + Q_COUNT);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const uint32_t rank = cluster_ctarank();
+  const unsigned pair = blockIdx.x >> 1, npairs = gridDim.x >> 1;
+  const bool has_res = p.epi.res != nullptr, has_pre = p.epi.pre != nullptr;
+  if (threadIdx.x == 0) {
+    for (int x = 0; x < Q_COUNT; ++x)
+      mbar_init(&bars[x], (x == Q_AEMPTY || x == Q_AEMPTY + 1) ? 16u : 1u);
+    fence_barrier_init();
+    tma_prefetch_desc(&tm_a);
+    tma_prefetch_desc(&tm_b);
+    tma_prefetch_desc(&io.out);
+  }
+  if (warp == 9) {
+    tmem_alloc_pair(tmem_slot, 512);
+    tmem_relinquish_pair();
+  }
+  tc_fence_before();
+  cluster_sync_all();  // barriers initialised in both CTAs before any remote use
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  bool ok = true;
+
+  if (warp == 8) {
+    if (lane == 0) {
+      int it = 0;
+      int issued[kPairStages] = {};
+      for (unsigned u = pair; ok && u < p.units; u += npairs) {
+        const unsigned t = u % p.tiles, part = u / p.tiles;
+        const int row = 256 * (int)(t / p.tiles_n) + 128 * (int)rank;
+        const int col = 256 * (int)(t % p.tiles_n) + 128 * (int)rank;
+        const int ks1 = (int)((long long)p.ksteps * (part + 1) / p.split);
+        for (int ks = (int)((long long)p.ksteps * part / p.split); ks < ks1; ++ks, ++it) {
+          const int st = it % kPairStages, use = it / kPairStages;
+          if (use > 0 && !mbar_wait(&bars[Q_EMPTY + st], (uint32_t)((use - 1) & 1))) {
+            ok = false;
+            break;
+          }
+          uint8_t* sa = smem + st * kPairStage;
+          uint8_t* sb = sa + kPairA;
+          if (rank == 0) mbar_arrive_expect_tx(&bars[Q_FULL + st], 2 * kPairStage);
+          const uint32_t full = smem_cluster_addr(&bars[Q_FULL + st], 0);
+          const int k = kKStep * ks;
+          if (p.a_mn) {
+            tma_load_half(sa, &tm_a, full, row, k);
+            tma_load_half(sa + 8192, &tm_a, full, row + 64, k);
+          } else {
+            tma_load_half(sa, &tm_a, full, k, row);
+          }
+          if (p.b_mn) {
+            tma_load_half(sb, &tm_b, full, col, k);
+            tma_load_half(sb + 8192, &tm_b, full, col + 64, k);
+          } else {
+            tma_load_half(sb, &tm_b, full, k, col);
+          }
+          ++issued[st];
+        }
+      }
+      // every copy into this CTA's ring has landed once its stage has been released
+      for (int st = 0; st < kPairStages; ++st)
+        if (issued[st] > 0) drain_wait(&bars[Q_EMPTY + st], (uint32_t)((issued[st] - 1) & 1));
+    }
+    __syncwarp();
+  } else if (warp == 9) {
+    if (rank == 0) {
+      const uint32_t idesc = idesc_f32acc(1, (uint32_t)p.a_mn, (uint32_t)p.b_mn, 256, 256);
+      int it = 0, lt = 0;
+      for (unsigned u = pair; ok && u < p.units; u += npairs, ++lt) {
+        const int acc = lt & 1, use = lt >> 1;
+        if (use > 0 && !mbar_wait_warp(&bars[Q_AEMPTY + acc], (uint32_t)((use - 1) & 1))) {
+          ok = false;
+          break;
+        }
+        tc_fence_after();
+        const unsigned part = u / p.tiles;
+        const int ks0 = (int)((long long)p.ksteps * part / p.split);
+        const int ks1 = (int)((long long)p.ksteps * (part + 1) / p.split);
+        const uint32_t td = tmem + (uint32_t)acc * 256;
+        for (int ks = ks0; ks < ks1; ++ks, ++it) {
+          const int st = it % kPairStages;
+          if (!mbar_wait_warp(&bars[Q_FULL + st], (uint32_t)((it / kPairStages) & 1))) {
+            ok = false;
+            break;
+          }
+          tc_fence_after();
+          if (elect_one()) {
+            const uint32_t sa = smem_u32(smem + st * kPairStage), sb = sa + kPairA;
+#pragma unroll
+            for (int kk = 0; kk < kKStep / 16; ++kk)
+              mma_bf16_ss_pair(td, operand_desc(p.a_mn, sa, kk), operand_desc(p.b_mn, sb, kk),
+                               idesc, (ks > ks0 || kk > 0) ? 1u : 0u);
+            mma_commit_pair(&bars[Q_EMPTY + st], 3);
+            if (ks == ks1 - 1) mma_commit_pair(&bars[Q_AFULL + acc], 3);
+          }
+          __syncwarp();
+        }
+      }
+      if (elect_one()) mma_commit_pair(&bars[Q_DRAIN], 3);
+      __syncwarp();
+      // both CTAs' epilogues have released every accumulator (their arrivals have landed)
+      if (lane == 0)
+        for (int acc = 0; acc < 2; ++acc) {
+          const int uses = (lt + 1 - acc) / 2;
+          if (uses > 0) drain_wait(&bars[Q_AEMPTY + acc], (uint32_t)((uses - 1) & 1));
+        }
+      __syncwarp();
+    }
+    // no product into either CTA's tensor memory is in flight past this point
+    if (lane == 0) drain_wait(&bars[Q_DRAIN], 0);
+    __syncwarp();
+  } else {
+    const uint32_t lanes = (uint32_t)(32 * (warp & 3)) << 16;
+    uint8_t* slots = staging + warp * 4 * kSlot;  // two for out and residual, two for pre
+    uint64_t* rbar = &bars[Q_RES + 2 * warp];
+    int lt = 0, chunk = 0, loads = 0;
+    for (unsigned u = pair; ok && u < p.units; u += npairs, ++lt) {
+      const unsigned t = u % p.tiles, part = u / p.tiles;
+      const int acc = lt & 1;
+      const long long row0 = 256ll * (t / p.tiles_n) + 128 * (int)rank + 32 * (warp & 3);
+      const long long col0 = 256ll * (t % p.tiles_n) + 128 * (warp >> 2);
+      int n = 0;  // chunks of 32 columns that are inside
+      if (row0 < p.rows && col0 < p.cols) {
+        const long long left = (p.cols - col0 + 31) / 32;
+        n = left < 4 ? (int)left : 4;
+      }
+      const bool res = has_res && p.split == 1;
+      auto load_res = [&](int c, int k) {  // chunk c of this tile into the slot of count k
+        bulk_wait_group_read0();           // no store still reads that slot
+        mbar_arrive_expect_tx(&rbar[k & 1], kSlot);
+        tma_load_tile(slots + (k & 1) * kSlot, &io.res, &rbar[k & 1], (int)col0 + 32 * c,
+                      (int)row0);
+      };
+      if (res && n > 0) {
+        if (lane == 0) load_res(0, chunk);
+        ++loads;
+      }
+      if (!mbar_wait_warp(&bars[Q_AFULL + acc], (uint32_t)((lt >> 1) & 1))) {
+        ok = false;
+        break;
+      }
+      tc_fence_after();
+#pragma unroll 1
+      for (int c = 0; c < n; ++c, ++chunk) {
+        if (res && c + 1 < n) {
+          if (lane == 0) load_res(c + 1, chunk + 1);
+          ++loads;
+        }
+        uint32_t a[32];
+        float v[32];
+        tmem_ld32(tmem + (uint32_t)acc * 256 + lanes + (uint32_t)(128 * (warp >> 2) + 32 * c), a);
+        const long long col = col0 + 32 * c;
+        if (p.epi.bias && p.split == 1) {
+#pragma unroll
+          for (int i = 0; i < 32; i += 4) {
+            float4 b = make_float4(0.f, 0.f, 0.f, 0.f);
+            if (col + i < p.cols) b = __ldg(reinterpret_cast<const float4*>(p.epi.bias + col + i));
+            v[i] = b.x; v[i + 1] = b.y; v[i + 2] = b.z; v[i + 3] = b.w;
+          }
+        } else {
+#pragma unroll
+          for (int i = 0; i < 32; ++i) v[i] = 0.f;
+        }
+        tmem_wait_ld();
+        if (c == n - 1) {  // the accumulator may take the next tile
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive_cluster(smem_cluster_addr(&bars[Q_AEMPTY + acc], 0));
+        }
+#pragma unroll
+        for (int i = 0; i < 32; ++i) v[i] += __uint_as_float(a[i]);
+        if (p.split > 1) {
+          if (row0 + lane < p.rows) {
+            float* dst = p.partial + ((long long)part * p.rows + row0 + lane) * p.cols + col;
+#pragma unroll
+            for (int i = 0; i < 32; i += 8)
+              if (col + i < p.cols) st_global_v8(dst + i, a + i);
+          }
+          continue;
+        }
+        // the stores that last read this count's slots (two chunks back) are done reading
+        if (lane == 0) bulk_wait_read_but_one();
+        __syncwarp();
+        const uint32_t so = smem_u32(slots + (chunk & 1) * kSlot);
+        if (has_pre) {
+#pragma unroll
+          for (int q = 0; q < 4; ++q)
+            st_shared_v4(so + 2 * kSlot + sw64(lane, q), pack_bf16x2(v[8 * q], v[8 * q + 1]),
+                         pack_bf16x2(v[8 * q + 2], v[8 * q + 3]),
+                         pack_bf16x2(v[8 * q + 4], v[8 * q + 5]),
+                         pack_bf16x2(v[8 * q + 6], v[8 * q + 7]));
+        }
+        with_act(p.epi.act, [&](auto k) {
+#pragma unroll
+          for (int i = 0; i < 32; ++i) v[i] = act_value<decltype(k)::value>(v[i]);
+        });
+        if (res) {
+          if (!mbar_wait_warp(&rbar[chunk & 1], (uint32_t)((chunk >> 1) & 1))) {
+            ok = false;
+            break;
+          }
+#pragma unroll
+          for (int q = 0; q < 4; ++q) {
+            const uint4 r = ld_shared_v4(so + sw64(lane, q));
+            const uint32_t w[4] = {r.x, r.y, r.z, r.w};
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              v[8 * q + 2 * i] += bf16_lo(w[i]);
+              v[8 * q + 2 * i + 1] += bf16_hi(w[i]);
+            }
+          }
+        }
+#pragma unroll
+        for (int q = 0; q < 4; ++q)
+          st_shared_v4(so + sw64(lane, q), pack_bf16x2(v[8 * q], v[8 * q + 1]),
+                       pack_bf16x2(v[8 * q + 2], v[8 * q + 3]),
+                       pack_bf16x2(v[8 * q + 4], v[8 * q + 5]),
+                       pack_bf16x2(v[8 * q + 6], v[8 * q + 7]));
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) {
+          tma_store_box(&io.out, slots + (chunk & 1) * kSlot, (int)col, (int)row0);
+          if (has_pre)
+            tma_store_box(&io.pre, slots + (2 + (chunk & 1)) * kSlot, (int)col, (int)row0);
+          tma_store_commit();
+        }
+      }
+      if (n == 0) {
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive_cluster(smem_cluster_addr(&bars[Q_AEMPTY + acc], 0));
+      }
+    }
+    if (lane == 0) {
+      // residual copies that a given-up wait left behind have landed (at most the last of
+      // each slot is unwaited), and every store has been done
+      if (!ok)
+        for (int k = loads > 2 ? loads - 2 : 0; k < loads; ++k)
+          drain_wait(&rbar[k & 1], (uint32_t)((k >> 1) & 1));
+      tma_store_wait_all();
+    }
+    __syncwarp();
+  }
+
+  tc_fence_before();
+  cluster_sync_all();  // both CTAs done with tensor memory and with each other's barriers
+  if (warp == 9) {
+    tc_fence_after();
+    tmem_dealloc_pair(tmem, 512);
+  }
+}
+
+// out from the partial sums of a split reduction, added in order, with the epilogue.
+// HBM- or L2-bound; a thread has 8 neighbouring columns.
+__global__ void __launch_bounds__(256)
+split_reduce_kernel(const float* __restrict__ partial, int split, long long rows, long long cols,
+                    const Epilogue epi) {
+  const long long units = rows * (cols / 8), per = cols / 8;
+  for (long long u = blockIdx.x * 256ll + threadIdx.x; u < units; u += gridDim.x * 256ll) {
+    const long long row = u / per, col = 8 * (u % per);
+    float v[8] = {};
+    for (int q = 0; q < split; ++q) {
+      const float4* src =
+          reinterpret_cast<const float4*>(partial + ((long long)q * rows + row) * cols + col);
+      const float4 x = __ldcs(src), y = __ldcs(src + 1);
+      v[0] += x.x; v[1] += x.y; v[2] += x.z; v[3] += x.w;
+      v[4] += y.x; v[5] += y.y; v[6] += y.z; v[7] += y.w;
+    }
+    finish8(v, epi, row, col);
+  }
+}
+
 // ---- host side --------------------------------------------------------------------------
 
 // Map over a stored matrix [outer][inner], rows ld elements apart; boxes of 64 inner x
@@ -311,6 +676,96 @@ bool make_map(CUtensorMap* m, const void* base, long long inner, long long outer
 bool operand_map(CUtensorMap* m, const __nv_bfloat16* p, long long ld, bool mn_major,
                  long long extent, long long R, int mn) {
   return mn_major ? make_map(m, p, extent, R, ld, 64) : make_map(m, p, R, extent, ld, (uint32_t)mn);
+}
+
+// Map of an output (or residual) in boxes of 32 columns x 32 rows, 64-byte swizzle.
+bool box_map(CUtensorMap* m, const __nv_bfloat16* p, long long rows, long long cols,
+             long long ld) {
+  EncodeTiledFn enc = get_encode_fn();
+  if (!enc) return false;
+  const cuuint64_t dims[2] = {(cuuint64_t)cols, (cuuint64_t)rows};
+  const cuuint64_t strides[1] = {(cuuint64_t)ld * 2};
+  const cuuint32_t box[2] = {32, 32};
+  const cuuint32_t estr[2] = {1, 1};
+  return enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<__nv_bfloat16*>(p), dims, strides,
+             box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_64B,
+             CU_TENSOR_MAP_L2_PROMOTION_NONE, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// CTA pairs that can be resident at once, looked up once per device.
+int pair_count(int sms) {
+  static std::atomic<int> cached[64];
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return 0;
+  int n = cached[dev].load(std::memory_order_relaxed);
+  if (n > 0) return n;
+  cudaLaunchConfig_t cfg;
+  memset(&cfg, 0, sizeof(cfg));
+  cfg.gridDim = dim3((unsigned)(sms & ~1));
+  cfg.blockDim = dim3(kPairThreads);
+  cfg.dynamicSmemBytes = kPairSmem;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeClusterDimension;
+  at[0].val.clusterDim.x = 2;
+  at[0].val.clusterDim.y = 1;
+  at[0].val.clusterDim.z = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = 1;
+  if (cudaOccupancyMaxActiveClusters(&n, linear_pair_kernel, &cfg) != cudaSuccess || n < 1) {
+    cudaGetLastError();
+    return 0;
+  }
+  cached[dev].store(n, std::memory_order_relaxed);
+  return n;
+}
+
+cudaError_t pair_launch(const GemmArgs& g, int split, float* partial, int sms,
+                        cudaStream_t stream) {
+  const int pairs = pair_count(sms);
+  if (pairs < 1) return cudaErrorLaunchOutOfResources;
+  CUtensorMap ma, mb;
+  PairMaps io;
+  if (!operand_map(&ma, g.a, g.lda, g.a_mn, g.P, g.R, 128) ||
+      !operand_map(&mb, g.b, g.ldb, g.b_mn, g.Q, g.R, 128) ||
+      !box_map(&io.out, g.out, g.P, g.Q, g.ldo))
+    return cudaErrorInvalidValue;
+  io.res = io.pre = io.out;
+  if (g.res && !box_map(&io.res, g.res, g.P, g.Q, g.ldr)) return cudaErrorInvalidValue;
+  if (g.pre && !box_map(&io.pre, g.pre, g.P, g.Q, g.ldp)) return cudaErrorInvalidValue;
+  PairParams p;
+  const long long tiles_n = (g.Q + 255) / 256, units = (g.P + 255) / 256 * tiles_n * split;
+  if (units >= (1ll << 31)) return cudaErrorInvalidValue;
+  p.tiles_n = (unsigned)tiles_n;
+  p.units = (unsigned)units;
+  p.tiles = p.units / (unsigned)split;
+  p.ksteps = (int)((g.R + kKStep - 1) / kKStep);
+  p.split = split;
+  p.a_mn = g.a_mn;
+  p.b_mn = g.b_mn;
+  p.rows = g.P;
+  p.cols = g.Q;
+  p.epi = Epilogue{g.bias, g.res, g.out, g.pre, g.ldr, g.ldo, g.ldp, g.act};
+  p.partial = partial;
+  cudaLaunchConfig_t cfg;
+  memset(&cfg, 0, sizeof(cfg));
+  cfg.gridDim = dim3(2 * (p.units < (unsigned)pairs ? p.units : (unsigned)pairs));
+  cfg.blockDim = dim3(kPairThreads);
+  cfg.dynamicSmemBytes = kPairSmem;
+  cfg.stream = stream;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeClusterDimension;
+  at[0].val.clusterDim.x = 2;
+  at[0].val.clusterDim.y = 1;
+  at[0].val.clusterDim.z = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = 1;
+  cudaError_t e = cudaLaunchKernelEx(&cfg, linear_pair_kernel, ma, mb, io, p);
+  if (e == cudaSuccess) e = cudaGetLastError();
+  if (e != cudaSuccess || split == 1) return e;
+  const long long blocks = (g.P * (g.Q / 8) + 255) / 256;
+  split_reduce_kernel<<<(unsigned)(blocks < 16ll * sms ? blocks : 16ll * sms), 256, 0, stream>>>(
+      partial, split, g.P, g.Q, p.epi);
+  return cudaGetLastError();
 }
 
 template <int BN, bool SWAP>
@@ -371,12 +826,43 @@ cudaError_t linear_set_attributes() {
   if (e == cudaSuccess) e = set_smem(linear_tile_kernel<32, true>, tile_smem(32));
   if (e == cudaSuccess) e = set_smem(linear_tile_kernel<64, true>, tile_smem(64));
   if (e == cudaSuccess) e = set_smem(linear_tile_kernel<128, false>, tile_smem(128));
+  if (e == cudaSuccess) e = set_smem(linear_pair_kernel, kPairSmem);
   return e;
 }
 
-size_t linear_gemm_scratch(long long, long long, long long, bool, int) { return 0; }
+namespace {
 
-cudaError_t linear_gemm_launch(const GemmArgs& g, void*, int sms, cudaStream_t stream) {
+// How a product is run. TUNE: thresholds from measurements.
+struct GemmPlan {
+  bool pair;
+  int split;  // blocks of a cluster, or parts of a pair launch
+};
+
+GemmPlan gemm_plan(long long P, long long Q, long long R, bool scratch, int sms) {
+  const long long ksteps = (R + kKStep - 1) / kKStep;
+  const long long small = (P + 127) / 128 * ((Q + 127) / 128);
+  const long long big = (P + 255) / 256 * ((Q + 255) / 256);
+  const int pairs = sms / 2;
+  if (P > 64 && small > sms) {
+    GemmPlan g{true, 1};
+    return g;
+  }
+  if (P > 64 && scratch && ksteps >= 32 && big * 2 <= pairs && small * 2 > sms / 2) {
+    long long s = pairs / big;
+    while (s > 1 && ksteps / s < 16) --s;
+    if (s > 1) return GemmPlan{true, (int)s};
+  }
+  return GemmPlan{false, tile_split(small, ksteps, sms)};
+}
+
+}  // namespace
+
+size_t linear_gemm_scratch(long long P, long long Q, long long R, bool scratch, int sms) {
+  const GemmPlan g = gemm_plan(P, Q, R, scratch, sms);
+  return g.pair && g.split > 1 ? (size_t)g.split * P * Q * 4 : 0;
+}
+
+cudaError_t linear_gemm_launch(const GemmArgs& g, void* scratch, int sms, cudaStream_t stream) {
   const long long ksteps = (g.R + kKStep - 1) / kKStep;
   // Few rows, stored along the reduction: the rows take the narrow side of the tile.
   if (g.P <= 64 && !g.a_mn) {
@@ -385,8 +871,9 @@ cudaError_t linear_gemm_launch(const GemmArgs& g, void*, int sms, cudaStream_t s
     if (g.P <= 32) return tile_launch<32, true>(g, s, stream);
     return tile_launch<64, true>(g, s, stream);
   }
-  const long long tiles = (g.P + 127) / 128 * ((g.Q + 127) / 128);
-  return tile_launch<128, false>(g, tile_split(tiles, ksteps, sms), stream);
+  const GemmPlan f = gemm_plan(g.P, g.Q, g.R, scratch != nullptr, sms);
+  if (f.pair) return pair_launch(g, f.split, static_cast<float*>(scratch), sms, stream);
+  return tile_launch<128, false>(g, f.split, stream);
 }
 
 // ---- the activation's gradient and the bias gradient --------------------------------------
