@@ -55,9 +55,12 @@ __device__ __forceinline__ void drain_wait(uint64_t* bar, uint32_t parity) {
 
 // Operand tile of `mn` rows or columns x 64 reduction elements in shared memory: K-major,
 // mn rows of 128 bytes; MN-major, blocks of 64 columns, each 64 rows of 128 bytes (8 KB).
-// Descriptor of its kk-th 16 reduction elements:
-__device__ __forceinline__ uint64_t operand_desc(bool mn_major, uint32_t base, int kk) {
-  return mn_major ? sdesc(base + (uint32_t)kk * 2048, 8192, 1024)
+// Descriptor of its kk-th 16 reduction elements. The storage order is a template parameter
+// of the kernels: the issuing thread's work per product has to stay below the product's
+// 128 tensor cycles.
+template <bool MN_MAJOR>
+__device__ __forceinline__ uint64_t operand_desc(uint32_t base, int kk) {
+  return MN_MAJOR ? sdesc(base + (uint32_t)kk * 2048, 8192, 1024)
                   : sdesc(base + (uint32_t)kk * 32, 16, 1024);
 }
 
@@ -100,7 +103,7 @@ __device__ __forceinline__ void finish8(float (&v)[8], const Epilogue& e, long l
   if (e.pre) *reinterpret_cast<uint4*>(e.pre + row * e.ldp + col) = pack8(v);
   with_act(e.act, [&](auto a) {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) v[i] = act_value<decltype(a)::value>(v[i]);
+    for (int i = 0; i < 8; i += 2) act_pair<decltype(a)::value>(v[i], v[i + 1]);
   });
   if (e.res) {
     const uint4 r = *reinterpret_cast<const uint4*>(e.res + row * e.ldr + col);
@@ -120,7 +123,6 @@ struct TileParams {
   unsigned tiles_b;  // BN-wide tiles along the B side
   int ksteps;        // of the whole reduction
   int split;         // blocks (cluster size) sharing the reduction
-  int a_mn, b_mn;
   long long rows, cols;  // of the output
   Epilogue epi;
 };
@@ -142,7 +144,7 @@ static_assert(16 * (128 + 4) * 4 <= tile_stages(16) * tile_stage_bytes(16), "til
 // in both cases, and a place from which the blocks of a cluster add their partial sums.
 // Bound by the stream of the weights with few rows: every block keeps its whole ring
 // (160 to 192 KB) in flight.
-template <int BN, bool SWAP>
+template <int BN, bool SWAP, bool A_MN, bool B_MN>
 __global__ void __launch_bounds__(kTileThreads, 1)
 linear_tile_kernel(const __grid_constant__ CUtensorMap tm_a,
                    const __grid_constant__ CUtensorMap tm_b, const TileParams p) {
@@ -190,13 +192,13 @@ linear_tile_kernel(const __grid_constant__ CUtensorMap tm_a,
         uint8_t* sb = sa + kABytes;
         const int k = kKStep * ks;
         mbar_arrive_expect_tx(&full[st], (uint32_t)kStage);
-        if (p.a_mn) {
+        if (A_MN) {
           tma_load_tile(sa, &tm_a, &full[st], a0, k);
           tma_load_tile(sa + 8192, &tm_a, &full[st], a0 + 64, k);
         } else {
           tma_load_tile(sa, &tm_a, &full[st], k, a0);
         }
-        if (BN >= 64 && p.b_mn) {
+        if (B_MN) {
 #pragma unroll
           for (int i = 0; i < (BN + 63) / 64; ++i)
             tma_load_tile(sb + 8192 * i, &tm_b, &full[st], b0 + 64 * i, k);
@@ -210,20 +212,21 @@ linear_tile_kernel(const __grid_constant__ CUtensorMap tm_a,
     }
     __syncwarp();
   } else if (warp == 5) {
-    const uint32_t idesc = idesc_f32acc(1, (uint32_t)p.a_mn, (uint32_t)p.b_mn, 128, BN);
-    for (int ks = ks0, it = 0; ks < ks1; ++ks, ++it) {
-      const int st = it % ST;
-      if (!mbar_wait_warp(&full[st], (uint32_t)((it / ST) & 1))) break;
+    constexpr uint32_t idesc = idesc_f32acc(1, A_MN, B_MN, 128, BN);
+    uint32_t st = 0, phase = 0;
+    for (int ks = ks0; ks < ks1; ++ks) {
+      if (!mbar_wait_warp(&full[st], phase)) break;
       tc_fence_after();
       if (elect_one()) {
         const uint32_t sa = smem_u32(smem + st * kStage), sb = sa + kABytes;
 #pragma unroll
         for (int kk = 0; kk < kKStep / 16; ++kk)
-          mma_bf16_ss(tmem, operand_desc(p.a_mn, sa, kk), operand_desc(p.b_mn, sb, kk), idesc,
-                      (it > 0 || kk > 0) ? 1u : 0u);
+          mma_bf16_ss(tmem, operand_desc<A_MN>(sa, kk), operand_desc<B_MN>(sb, kk), idesc,
+                      (ks > ks0 || kk > 0) ? 1u : 0u);
         mma_commit(&empty[st]);
       }
       __syncwarp();
+      if (++st == ST) st = 0, phase ^= 1;
     }
     if (elect_one()) mma_commit(acc);  // all products done: sums complete, ring free
     __syncwarp();
@@ -302,7 +305,6 @@ struct PairParams {
   unsigned tiles_n, tiles;  // of 256 columns; in all
   unsigned units;           // tiles * split
   int ksteps, split;
-  int a_mn, b_mn;
   long long rows, cols;
   Epilogue epi;    // out, res and pre go through tensor maps
   float* partial;  // split > 1: [split][rows][cols]
@@ -312,22 +314,26 @@ struct PairMaps {
   CUtensorMap out, res, pre;  // boxes of 32 columns x 32 rows, 64-byte swizzle
 };
 
-constexpr int kPairThreads = 320;
+constexpr int kEpiWarps = 8;  // of a CTA: four lane quarters x two column halves
+constexpr int kPairThreads = 32 * (kEpiWarps + 2);
 constexpr int kPairStages = 5;
 constexpr int kPairA = 16384, kPairStage = 2 * kPairA;  // this CTA's half of A and of B
 constexpr int kSlot = 2048;                             // 32 rows x 64 bytes
-constexpr int kPairStaging = 8 * 4 * kSlot;
+constexpr int kSlots = 4;                               // of an epilogue warp
+constexpr int kPairStaging = kEpiWarps * kSlots * kSlot;
 enum {
   Q_FULL = 0,
   Q_EMPTY = Q_FULL + kPairStages,
   Q_AFULL = Q_EMPTY + kPairStages,
   Q_AEMPTY = Q_AFULL + 2,
   Q_DRAIN = Q_AEMPTY + 2,
-  Q_RES = Q_DRAIN + 1,  // two per epilogue warp
-  Q_COUNT = Q_RES + 16
+  Q_RES = Q_DRAIN + 1,  // one per staging slot
+  Q_COUNT = Q_RES + kSlots * kEpiWarps
 };
-static_assert(Q_COUNT * 8 + 4 <= 256, "barrier area");
-constexpr int kPairSmem = kPairStages * kPairStage + kPairStaging + 256 + 1024;
+constexpr int kPairBars = 512;
+static_assert(Q_COUNT * 8 + 4 <= kPairBars, "barrier area");
+constexpr int kPairSmem = kPairStages * kPairStage + kPairStaging + kPairBars + 1024;
+static_assert(kPairSmem <= 232448, "shared memory of a block");
 
 // A copy into this CTA's shared memory that completes on a barrier of the pair (address in
 // the cluster's window).
@@ -349,9 +355,10 @@ __device__ __forceinline__ void tma_store_box(const CUtensorMap* m, const void* 
       : "memory");
 }
 
-// Until at most one of this thread's bulk store groups still reads shared memory.
-__device__ __forceinline__ void bulk_wait_read_but_one() {
-  asm volatile("cp.async.bulk.wait_group.read 1;" ::: "memory");
+// Until at most N of this thread's bulk store groups still read shared memory.
+template <int N>
+__device__ __forceinline__ void bulk_wait_read_but() {
+  asm volatile("cp.async.bulk.wait_group.read %0;" ::"n"(N) : "memory");
 }
 
 __device__ __forceinline__ uint4 ld_shared_v4(uint32_t addr) {
@@ -373,8 +380,11 @@ __device__ __forceinline__ uint32_t sw64(uint32_t r, uint32_t u) {
 // N = 256, K = 16 each). Each k-step of 64 brings 128 rows (columns) of A and of B into
 // each CTA, both CTAs' copies completing on the even CTA's barrier. The epilogue takes 32
 // columns at a time: accumulator -> registers -> swizzled staging slot -> TMA store, which
-// writes whole sectors and clips at the edges; a residual comes into the same slot by a
-// TMA load one step ahead and is replaced by the output in place.
+// writes whole sectors and clips at the edges; a residual comes into the same slot by a TMA
+// load ahead of time and is replaced by the output in place. A warp has four slots, so that
+// stores and loads are in flight while it works on the next columns: the chunks take them
+// in turn, or, with a pre-activation to write, two of them, the pre-activation the others.
+template <bool A_MN, bool B_MN>
 __global__ void __launch_bounds__(kPairThreads, 1)
 linear_pair_kernel(const __grid_constant__ CUtensorMap tm_a,
                    const __grid_constant__ CUtensorMap tm_b,
@@ -391,13 +401,13 @@ linear_pair_kernel(const __grid_constant__ CUtensorMap tm_a,
   const bool has_res = p.epi.res != nullptr, has_pre = p.epi.pre != nullptr;
   if (threadIdx.x == 0) {
     for (int x = 0; x < Q_COUNT; ++x)
-      mbar_init(&bars[x], (x == Q_AEMPTY || x == Q_AEMPTY + 1) ? 16u : 1u);
+      mbar_init(&bars[x], (x == Q_AEMPTY || x == Q_AEMPTY + 1) ? 2u * kEpiWarps : 1u);
     fence_barrier_init();
     tma_prefetch_desc(&tm_a);
     tma_prefetch_desc(&tm_b);
     tma_prefetch_desc(&io.out);
   }
-  if (warp == 9) {
+  if (warp == kEpiWarps + 1) {
     tmem_alloc_pair(tmem_slot, 512);
     tmem_relinquish_pair();
   }
@@ -407,7 +417,7 @@ linear_pair_kernel(const __grid_constant__ CUtensorMap tm_a,
   const uint32_t tmem = *tmem_slot;
   bool ok = true;
 
-  if (warp == 8) {
+  if (warp == kEpiWarps) {
     if (lane == 0) {
       int it = 0;
       int issued[kPairStages] = {};
@@ -427,13 +437,13 @@ linear_pair_kernel(const __grid_constant__ CUtensorMap tm_a,
           if (rank == 0) mbar_arrive_expect_tx(&bars[Q_FULL + st], 2 * kPairStage);
           const uint32_t full = smem_cluster_addr(&bars[Q_FULL + st], 0);
           const int k = kKStep * ks;
-          if (p.a_mn) {
+          if (A_MN) {
             tma_load_half(sa, &tm_a, full, row, k);
             tma_load_half(sa + 8192, &tm_a, full, row + 64, k);
           } else {
             tma_load_half(sa, &tm_a, full, k, row);
           }
-          if (p.b_mn) {
+          if (B_MN) {
             tma_load_half(sb, &tm_b, full, col, k);
             tma_load_half(sb + 8192, &tm_b, full, col + 64, k);
           } else {
@@ -447,10 +457,11 @@ linear_pair_kernel(const __grid_constant__ CUtensorMap tm_a,
         if (issued[st] > 0) drain_wait(&bars[Q_EMPTY + st], (uint32_t)((issued[st] - 1) & 1));
     }
     __syncwarp();
-  } else if (warp == 9) {
+  } else if (warp == kEpiWarps + 1) {
     if (rank == 0) {
-      const uint32_t idesc = idesc_f32acc(1, (uint32_t)p.a_mn, (uint32_t)p.b_mn, 256, 256);
-      int it = 0, lt = 0;
+      constexpr uint32_t idesc = idesc_f32acc(1, A_MN, B_MN, 256, 256);
+      uint32_t st = 0, phase = 0;
+      int lt = 0;
       for (unsigned u = pair; ok && u < p.units; u += npairs, ++lt) {
         const int acc = lt & 1, use = lt >> 1;
         if (use > 0 && !mbar_wait_warp(&bars[Q_AEMPTY + acc], (uint32_t)((use - 1) & 1))) {
@@ -462,9 +473,8 @@ linear_pair_kernel(const __grid_constant__ CUtensorMap tm_a,
         const int ks0 = (int)((long long)p.ksteps * part / p.split);
         const int ks1 = (int)((long long)p.ksteps * (part + 1) / p.split);
         const uint32_t td = tmem + (uint32_t)acc * 256;
-        for (int ks = ks0; ks < ks1; ++ks, ++it) {
-          const int st = it % kPairStages;
-          if (!mbar_wait_warp(&bars[Q_FULL + st], (uint32_t)((it / kPairStages) & 1))) {
+        for (int ks = ks0; ks < ks1; ++ks) {
+          if (!mbar_wait_warp(&bars[Q_FULL + st], phase)) {
             ok = false;
             break;
           }
@@ -473,12 +483,13 @@ linear_pair_kernel(const __grid_constant__ CUtensorMap tm_a,
             const uint32_t sa = smem_u32(smem + st * kPairStage), sb = sa + kPairA;
 #pragma unroll
             for (int kk = 0; kk < kKStep / 16; ++kk)
-              mma_bf16_ss_pair(td, operand_desc(p.a_mn, sa, kk), operand_desc(p.b_mn, sb, kk),
-                               idesc, (ks > ks0 || kk > 0) ? 1u : 0u);
+              mma_bf16_ss_pair(td, operand_desc<A_MN>(sa, kk), operand_desc<B_MN>(sb, kk), idesc,
+                               (ks > ks0 || kk > 0) ? 1u : 0u);
             mma_commit_pair(&bars[Q_EMPTY + st], 3);
             if (ks == ks1 - 1) mma_commit_pair(&bars[Q_AFULL + acc], 3);
           }
           __syncwarp();
+          if (++st == kPairStages) st = 0, phase ^= 1;
         }
       }
       if (elect_one()) mma_commit_pair(&bars[Q_DRAIN], 3);
@@ -496,8 +507,12 @@ linear_pair_kernel(const __grid_constant__ CUtensorMap tm_a,
     __syncwarp();
   } else {
     const uint32_t lanes = (uint32_t)(32 * (warp & 3)) << 16;
-    uint8_t* slots = staging + warp * 4 * kSlot;  // two for out and residual, two for pre
-    uint64_t* rbar = &bars[Q_RES + 2 * warp];
+    uint8_t* slots = staging + warp * kSlots * kSlot;
+    uint64_t* rbar = &bars[Q_RES + kSlots * warp];
+    const bool res = has_res && p.split == 1;
+    // chunk k of this warp (counted over its tiles) has slot k & mask, for the
+    // (k >> turns)-th time; a residual is loaded `ahead` chunks before its use
+    const int turns = has_pre ? 1 : 2, mask = (1 << turns) - 1, ahead = turns;
     int lt = 0, chunk = 0, loads = 0;
     for (unsigned u = pair; ok && u < p.units; u += npairs, ++lt) {
       const unsigned t = u % p.tiles, part = u / p.tiles;
@@ -509,17 +524,22 @@ linear_pair_kernel(const __grid_constant__ CUtensorMap tm_a,
         const long long left = (p.cols - col0 + 31) / 32;
         n = left < 4 ? (int)left : 4;
       }
-      const bool res = has_res && p.split == 1;
-      auto load_res = [&](int c, int k) {  // chunk c of this tile into the slot of count k
-        bulk_wait_group_read0();           // no store still reads that slot
-        mbar_arrive_expect_tx(&rbar[k & 1], kSlot);
-        tma_load_tile(slots + (k & 1) * kSlot, &io.res, &rbar[k & 1], (int)col0 + 32 * c,
-                      (int)row0);
+      auto load_res = [&](int c, int k) {  // chunk c of this tile, the k-th of this warp
+        uint64_t* bar = &rbar[k & mask];
+        mbar_arrive_expect_tx(bar, kSlot);
+        tma_load_tile(slots + (k & mask) * kSlot, &io.res, bar, (int)col0 + 32 * c, (int)row0);
       };
       if (res && n > 0) {
-        if (lane == 0) load_res(0, chunk);
-        ++loads;
+        if (lane == 0) {
+          bulk_wait_read_but<1>();  // frees the slots of the next one or two chunks
+          load_res(0, chunk);
+          if (ahead == 2 && n > 1) load_res(1, chunk + 1);
+        }
+        loads = chunk + (ahead < n ? ahead : n);
       }
+      // this tile's bias into L1 while its products run
+      if (p.epi.bias && p.split == 1 && lane < 4 && col0 + 32 * lane < p.cols)
+        asm volatile("prefetch.global.L1 [%0];" ::"l"(p.epi.bias + col0 + 32 * lane));
       if (!mbar_wait_warp(&bars[Q_AFULL + acc], (uint32_t)((lt >> 1) & 1))) {
         ok = false;
         break;
@@ -527,10 +547,6 @@ linear_pair_kernel(const __grid_constant__ CUtensorMap tm_a,
       tc_fence_after();
 #pragma unroll 1
       for (int c = 0; c < n; ++c, ++chunk) {
-        if (res && c + 1 < n) {
-          if (lane == 0) load_res(c + 1, chunk + 1);
-          ++loads;
-        }
         uint32_t a[32];
         float v[32];
         tmem_ld32(tmem + (uint32_t)acc * 256 + lanes + (uint32_t)(128 * (warp >> 2) + 32 * c), a);
@@ -546,14 +562,29 @@ linear_pair_kernel(const __grid_constant__ CUtensorMap tm_a,
 #pragma unroll
           for (int i = 0; i < 32; ++i) v[i] = 0.f;
         }
+        if (lane == 0) {
+          // a residual further on, into a slot whose last store has been read; and the
+          // slots written now (their stores are further back)
+          if (turns == 2) {
+            if (res)
+              bulk_wait_read_but<1>();
+            else
+              bulk_wait_read_but<3>();
+          } else {
+            if (res)
+              bulk_wait_read_but<0>();
+            else
+              bulk_wait_read_but<1>();
+          }
+          if (res && c + ahead < n) load_res(c + ahead, chunk + ahead);
+        }
+        if (res && c + ahead < n) loads = chunk + ahead + 1;
         tmem_wait_ld();
         if (c == n - 1) {  // the accumulator may take the next tile
           tc_fence_before();
           __syncwarp();
           if (lane == 0) mbar_arrive_cluster(smem_cluster_addr(&bars[Q_AEMPTY + acc], 0));
         }
-#pragma unroll
-        for (int i = 0; i < 32; ++i) v[i] += __uint_as_float(a[i]);
         if (p.split > 1) {
           if (row0 + lane < p.rows) {
             float* dst = p.partial + ((long long)part * p.rows + row0 + lane) * p.cols + col;
@@ -563,10 +594,10 @@ linear_pair_kernel(const __grid_constant__ CUtensorMap tm_a,
           }
           continue;
         }
-        // the stores that last read this count's slots (two chunks back) are done reading
-        if (lane == 0) bulk_wait_read_but_one();
+#pragma unroll
+        for (int i = 0; i < 32; ++i) v[i] += __uint_as_float(a[i]);
         __syncwarp();
-        const uint32_t so = smem_u32(slots + (chunk & 1) * kSlot);
+        const uint32_t so = smem_u32(slots + (chunk & mask) * kSlot);
         if (has_pre) {
 #pragma unroll
           for (int q = 0; q < 4; ++q)
@@ -577,10 +608,10 @@ linear_pair_kernel(const __grid_constant__ CUtensorMap tm_a,
         }
         with_act(p.epi.act, [&](auto k) {
 #pragma unroll
-          for (int i = 0; i < 32; ++i) v[i] = act_value<decltype(k)::value>(v[i]);
+          for (int i = 0; i < 32; i += 2) act_pair<decltype(k)::value>(v[i], v[i + 1]);
         });
         if (res) {
-          if (!mbar_wait_warp(&rbar[chunk & 1], (uint32_t)((chunk >> 1) & 1))) {
+          if (!mbar_wait_warp(&rbar[chunk & mask], (uint32_t)((chunk >> turns) & 1))) {
             ok = false;
             break;
           }
@@ -604,9 +635,9 @@ linear_pair_kernel(const __grid_constant__ CUtensorMap tm_a,
         fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0) {
-          tma_store_box(&io.out, slots + (chunk & 1) * kSlot, (int)col, (int)row0);
+          tma_store_box(&io.out, slots + (chunk & mask) * kSlot, (int)col, (int)row0);
           if (has_pre)
-            tma_store_box(&io.pre, slots + (2 + (chunk & 1)) * kSlot, (int)col, (int)row0);
+            tma_store_box(&io.pre, slots + (2 + (chunk & mask)) * kSlot, (int)col, (int)row0);
           tma_store_commit();
         }
       }
@@ -617,11 +648,11 @@ linear_pair_kernel(const __grid_constant__ CUtensorMap tm_a,
       }
     }
     if (lane == 0) {
-      // residual copies that a given-up wait left behind have landed (at most the last of
-      // each slot is unwaited), and every store has been done
+      // residual copies that a given-up wait left behind have landed, and every store has
+      // been done
       if (!ok)
-        for (int k = loads > 2 ? loads - 2 : 0; k < loads; ++k)
-          drain_wait(&rbar[k & 1], (uint32_t)((k >> 1) & 1));
+        for (int k = loads > mask + 1 ? loads - mask - 1 : 0; k < loads; ++k)
+          drain_wait(&rbar[k & mask], (uint32_t)((k >> turns) & 1));
       tma_store_wait_all();
     }
     __syncwarp();
@@ -629,7 +660,7 @@ linear_pair_kernel(const __grid_constant__ CUtensorMap tm_a,
 
   tc_fence_before();
   cluster_sync_all();  // both CTAs done with tensor memory and with each other's barriers
-  if (warp == 9) {
+  if (warp == kEpiWarps + 1) {
     tc_fence_after();
     tmem_dealloc_pair(tmem, 512);
   }
@@ -657,39 +688,34 @@ split_reduce_kernel(const float* __restrict__ partial, int split, long long rows
 
 // ---- host side --------------------------------------------------------------------------
 
-// Map over a stored matrix [outer][inner], rows ld elements apart; boxes of 64 inner x
-// box_outer outer elements, 128-byte swizzle. Reads outside the matrix give zeros.
+// Map over a stored matrix [outer][inner], rows ld elements apart; boxes of 64 (swizzle
+// 128 bytes) or 32 (64 bytes) inner x box_outer outer elements. Reads outside the matrix
+// give zeros, stores outside it are dropped.
 bool make_map(CUtensorMap* m, const void* base, long long inner, long long outer, long long ld,
-              uint32_t box_outer) {
+              uint32_t box_inner, uint32_t box_outer) {
   EncodeTiledFn enc = get_encode_fn();
   if (!enc) return false;
   const cuuint64_t dims[2] = {(cuuint64_t)inner, (cuuint64_t)outer};
   const cuuint64_t strides[1] = {(cuuint64_t)ld * 2};
-  const cuuint32_t box[2] = {64, box_outer};
+  const cuuint32_t box[2] = {box_inner, box_outer};
   const cuuint32_t estr[2] = {1, 1};
   return enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(base), dims, strides, box,
-             estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+             estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+             box_inner == 64 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
              CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 // Map of an operand whose tile is `mn` rows or columns wide.
 bool operand_map(CUtensorMap* m, const __nv_bfloat16* p, long long ld, bool mn_major,
                  long long extent, long long R, int mn) {
-  return mn_major ? make_map(m, p, extent, R, ld, 64) : make_map(m, p, R, extent, ld, (uint32_t)mn);
+  return mn_major ? make_map(m, p, extent, R, ld, 64, 64)
+                  : make_map(m, p, R, extent, ld, 64, (uint32_t)mn);
 }
 
 // Map of an output (or residual) in boxes of 32 columns x 32 rows, 64-byte swizzle.
 bool box_map(CUtensorMap* m, const __nv_bfloat16* p, long long rows, long long cols,
              long long ld) {
-  EncodeTiledFn enc = get_encode_fn();
-  if (!enc) return false;
-  const cuuint64_t dims[2] = {(cuuint64_t)cols, (cuuint64_t)rows};
-  const cuuint64_t strides[1] = {(cuuint64_t)ld * 2};
-  const cuuint32_t box[2] = {32, 32};
-  const cuuint32_t estr[2] = {1, 1};
-  return enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<__nv_bfloat16*>(p), dims, strides,
-             box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_64B,
-             CU_TENSOR_MAP_L2_PROMOTION_NONE, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+  return make_map(m, p, cols, rows, ld, 32, 32);
 }
 
 // CTA pairs that can be resident at once, looked up once per device.
@@ -711,7 +737,7 @@ int pair_count(int sms) {
   at[0].val.clusterDim.z = 1;
   cfg.attrs = at;
   cfg.numAttrs = 1;
-  if (cudaOccupancyMaxActiveClusters(&n, linear_pair_kernel, &cfg) != cudaSuccess || n < 1) {
+  if (cudaOccupancyMaxActiveClusters(&n, linear_pair_kernel<false, true>, &cfg) != cudaSuccess || n < 1) {
     cudaGetLastError();
     return 0;
   }
@@ -740,8 +766,6 @@ cudaError_t pair_launch(const GemmArgs& g, int split, float* partial, int sms,
   p.tiles = p.units / (unsigned)split;
   p.ksteps = (int)((g.R + kKStep - 1) / kKStep);
   p.split = split;
-  p.a_mn = g.a_mn;
-  p.b_mn = g.b_mn;
   p.rows = g.P;
   p.cols = g.Q;
   p.epi = Epilogue{g.bias, g.res, g.out, g.pre, g.ldr, g.ldo, g.ldp, g.act};
@@ -759,7 +783,9 @@ cudaError_t pair_launch(const GemmArgs& g, int split, float* partial, int sms,
   at[0].val.clusterDim.z = 1;
   cfg.attrs = at;
   cfg.numAttrs = 1;
-  cudaError_t e = cudaLaunchKernelEx(&cfg, linear_pair_kernel, ma, mb, io, p);
+  cudaError_t e = g.a_mn   ? cudaLaunchKernelEx(&cfg, linear_pair_kernel<true, true>, ma, mb, io, p)
+                  : g.b_mn ? cudaLaunchKernelEx(&cfg, linear_pair_kernel<false, true>, ma, mb, io, p)
+                           : cudaLaunchKernelEx(&cfg, linear_pair_kernel<false, false>, ma, mb, io, p);
   if (e == cudaSuccess) e = cudaGetLastError();
   if (e != cudaSuccess || split == 1) return e;
   const long long blocks = (g.P * (g.Q / 8) + 255) / 256;
@@ -768,7 +794,7 @@ cudaError_t pair_launch(const GemmArgs& g, int split, float* partial, int sms,
   return cudaGetLastError();
 }
 
-template <int BN, bool SWAP>
+template <int BN, bool SWAP, bool A_MN, bool B_MN>
 cudaError_t tile_launch(const GemmArgs& g, int split, cudaStream_t stream) {
   const long long a_extent = SWAP ? g.Q : g.P, b_extent = SWAP ? g.P : g.Q;
   CUtensorMap ma, mb;
@@ -784,8 +810,6 @@ cudaError_t tile_launch(const GemmArgs& g, int split, cudaStream_t stream) {
   p.tiles_b = (unsigned)tiles_b;
   p.ksteps = (int)((g.R + kKStep - 1) / kKStep);
   p.split = split;
-  p.a_mn = SWAP ? g.b_mn : g.a_mn;
-  p.b_mn = SWAP ? g.a_mn : g.b_mn;
   p.rows = g.P;
   p.cols = g.Q;
   p.epi = Epilogue{g.bias, g.res, g.out, g.pre, g.ldr, g.ldo, g.ldp, g.act};
@@ -802,7 +826,7 @@ cudaError_t tile_launch(const GemmArgs& g, int split, cudaStream_t stream) {
   at[0].val.clusterDim.z = 1;
   cfg.attrs = at;
   cfg.numAttrs = split > 1 ? 1 : 0;
-  const cudaError_t e = cudaLaunchKernelEx(&cfg, linear_tile_kernel<BN, SWAP>, ma, mb, p);
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, linear_tile_kernel<BN, SWAP, A_MN, B_MN>, ma, mb, p);
   return e != cudaSuccess ? e : cudaGetLastError();
 }
 
@@ -822,11 +846,22 @@ cudaError_t set_smem(K* kernel, int bytes) {
 }  // namespace
 
 cudaError_t linear_set_attributes() {
-  cudaError_t e = set_smem(linear_tile_kernel<16, true>, tile_smem(16));
-  if (e == cudaSuccess) e = set_smem(linear_tile_kernel<32, true>, tile_smem(32));
-  if (e == cudaSuccess) e = set_smem(linear_tile_kernel<64, true>, tile_smem(64));
-  if (e == cudaSuccess) e = set_smem(linear_tile_kernel<128, false>, tile_smem(128));
-  if (e == cudaSuccess) e = set_smem(linear_pair_kernel, kPairSmem);
+  cudaError_t e = cudaSuccess;
+  auto set = [&](auto* kernel, int bytes) {
+    if (e == cudaSuccess) e = set_smem(kernel, bytes);
+  };
+  set(linear_tile_kernel<16, true, true, false>, tile_smem(16));
+  set(linear_tile_kernel<16, true, false, false>, tile_smem(16));
+  set(linear_tile_kernel<32, true, true, false>, tile_smem(32));
+  set(linear_tile_kernel<32, true, false, false>, tile_smem(32));
+  set(linear_tile_kernel<64, true, true, false>, tile_smem(64));
+  set(linear_tile_kernel<64, true, false, false>, tile_smem(64));
+  set(linear_tile_kernel<128, false, false, true>, tile_smem(128));
+  set(linear_tile_kernel<128, false, false, false>, tile_smem(128));
+  set(linear_tile_kernel<128, false, true, true>, tile_smem(128));
+  set(linear_pair_kernel<false, true>, kPairSmem);
+  set(linear_pair_kernel<false, false>, kPairSmem);
+  set(linear_pair_kernel<true, true>, kPairSmem);
   return e;
 }
 
@@ -862,18 +897,28 @@ size_t linear_gemm_scratch(long long P, long long Q, long long R, bool scratch, 
   return g.pair && g.split > 1 ? (size_t)g.split * P * Q * 4 : 0;
 }
 
+// The products there are: x W (A along the reduction, B across it), d W^T (both along),
+// x^T d (both across).
 cudaError_t linear_gemm_launch(const GemmArgs& g, void* scratch, int sms, cudaStream_t stream) {
+  if (g.a_mn && !g.b_mn) return cudaErrorInvalidValue;
   const long long ksteps = (g.R + kKStep - 1) / kKStep;
   // Few rows, stored along the reduction: the rows take the narrow side of the tile.
   if (g.P <= 64 && !g.a_mn) {
     const int s = tile_split((g.Q + 127) / 128, ksteps, sms);
-    if (g.P <= 16) return tile_launch<16, true>(g, s, stream);
-    if (g.P <= 32) return tile_launch<32, true>(g, s, stream);
-    return tile_launch<64, true>(g, s, stream);
+    if (g.P <= 16)
+      return g.b_mn ? tile_launch<16, true, true, false>(g, s, stream)
+                    : tile_launch<16, true, false, false>(g, s, stream);
+    if (g.P <= 32)
+      return g.b_mn ? tile_launch<32, true, true, false>(g, s, stream)
+                    : tile_launch<32, true, false, false>(g, s, stream);
+    return g.b_mn ? tile_launch<64, true, true, false>(g, s, stream)
+                  : tile_launch<64, true, false, false>(g, s, stream);
   }
   const GemmPlan f = gemm_plan(g.P, g.Q, g.R, scratch != nullptr, sms);
   if (f.pair) return pair_launch(g, f.split, static_cast<float*>(scratch), sms, stream);
-  return tile_launch<128, false>(g, f.split, stream);
+  return g.a_mn   ? tile_launch<128, false, true, true>(g, f.split, stream)
+         : g.b_mn ? tile_launch<128, false, false, true>(g, f.split, stream)
+                  : tile_launch<128, false, false, false>(g, f.split, stream);
 }
 
 // ---- the activation's gradient and the bias gradient --------------------------------------
@@ -882,12 +927,14 @@ namespace {
 
 constexpr int kActCols = 256;  // columns of a block: 32 lanes x 8
 constexpr int kActWarps = 8;
+constexpr int kBatch = 4;
+constexpr int kActBlocks = 3;  // resident per SM
 
 // dpre = dy act'(pre), one 16-byte piece of a row per thread and step, and the column
 // sums of dpre before its rounding (fp32, one row of `part` per row chunk). HBM-bound:
 // dy and pre read once, dpre written once.
 template <int ACT>
-__global__ void __launch_bounds__(32 * kActWarps)
+__global__ void __launch_bounds__(32 * kActWarps, kActBlocks)
 act_grad_kernel(const __nv_bfloat16* __restrict__ dy, long long lddy,
                 const __nv_bfloat16* __restrict__ pre, long long ldp,
                 __nv_bfloat16* __restrict__ dpre, float* __restrict__ part, long long M, int N) {
@@ -898,29 +945,41 @@ act_grad_kernel(const __nv_bfloat16* __restrict__ dy, long long lddy,
   const long long r0 = M * blockIdx.y / gridDim.y, r1 = M * (blockIdx.y + 1) / gridDim.y;
   float s[8] = {};
   if (in) {
-#pragma unroll 4
-    for (long long r = r0 + warp; r < r1; r += kActWarps) {
-      const uint4 g = __ldg(reinterpret_cast<const uint4*>(dy + r * lddy + col));
-      const uint32_t gw[4] = {g.x, g.y, g.z, g.w};
-      float d[8];
+    // kBatch rows' loads in flight before the first is used
+    for (long long r = r0 + warp; r < r1; r += kBatch * kActWarps) {
+      uint4 g[kBatch], z[kBatch];
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        d[2 * i] = bf16_lo(gw[i]);
-        d[2 * i + 1] = bf16_hi(gw[i]);
+      for (int k = 0; k < kBatch; ++k) {
+        const long long rk = r + k * kActWarps;
+        if (rk < r1) {
+          g[k] = __ldcs(reinterpret_cast<const uint4*>(dy + rk * lddy + col));
+          if (ACT != kActNone) z[k] = __ldcs(reinterpret_cast<const uint4*>(pre + rk * ldp + col));
+        }
       }
-      if (ACT != kActNone) {
-        const uint4 z = __ldg(reinterpret_cast<const uint4*>(pre + r * ldp + col));
-        const uint32_t zw[4] = {z.x, z.y, z.z, z.w};
+#pragma unroll
+      for (int k = 0; k < kBatch; ++k) {
+        const long long rk = r + k * kActWarps;
+        if (rk >= r1) break;
+        const uint32_t gw[4] = {g[k].x, g[k].y, g[k].z, g[k].w};
+        const uint32_t zw[4] = {z[k].x, z[k].y, z[k].z, z[k].w};
+        float d[8];
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          d[2 * i] *= act_deriv<ACT>(bf16_lo(zw[i]));
-          d[2 * i + 1] *= act_deriv<ACT>(bf16_hi(zw[i]));
+          d[2 * i] = bf16_lo(gw[i]);
+          d[2 * i + 1] = bf16_hi(gw[i]);
+          if (ACT != kActNone) {
+            float a = bf16_lo(zw[i]), b = bf16_hi(zw[i]);
+            act_deriv_pair<ACT>(a, b);
+            d[2 * i] *= a;
+            d[2 * i + 1] *= b;
+          }
+          s[2 * i] += d[2 * i];
+          s[2 * i + 1] += d[2 * i + 1];
         }
-        // bf16 because the tensor cores read it: 2^-9 relative, as every operand's rounding
-        *reinterpret_cast<uint4*>(dpre + r * (long long)N + col) = pack8(d);
+        // bf16 because the tensor cores read it: 2^-8 relative at most, as every operand
+        if (ACT != kActNone)
+          *reinterpret_cast<uint4*>(dpre + rk * (long long)N + col) = pack8(d);
       }
-#pragma unroll
-      for (int i = 0; i < 8; ++i) s[i] += d[i];
     }
   }
   if (!part) return;
@@ -958,10 +1017,10 @@ __global__ void __launch_bounds__(256) colsum_kernel(const ColsumArgs a) {
 }  // namespace
 
 int act_grad_chunks(long long M, int N, int sms) {
-  // about eight blocks per SM, 8 rows per warp at least
+  // one wave of resident blocks, one batch of rows per warp at least
   const long long across = (N + kActCols - 1) / kActCols;
-  long long c = (8ll * sms + across - 1) / across;
-  const long long most = (M + 8 * kActWarps - 1) / (8 * kActWarps);
+  long long c = (long long)kActBlocks * sms / across;
+  const long long most = (M + kBatch * kActWarps - 1) / (kBatch * kActWarps);
   c = c < most ? c : most;
   return (int)(c < 1 ? 1 : (c > 65535 ? 65535 : c));
 }

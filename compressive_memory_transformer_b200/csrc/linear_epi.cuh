@@ -1,45 +1,112 @@
 // linear_epi.cuh — the activations of the matrix products' epilogues and of their
-// gradients, in fp32.
+// gradients, in fp32. Forward activations work on two values at a time: their multiplies
+// and adds are packed (f32x2), which leaves the two special-function instructions per
+// value (an exponential and a reciprocal, 16 per SM and cycle) as what bounds them; a
+// 1024-long product's epilogue has a quarter of a cycle per output and SM in all.
 #pragma once
 #include <cuda_bf16.h>
+#include <type_traits>
 
 #include "block_ops.h"
+#include "sm100.cuh"
 
 namespace infini {
 
-// relu(v) = max(v, 0) (a NaN stays one); silu(v) = v / (1 + e^-v);
-// gelu(v) = v Phi(v) = v (1 + erf(v / sqrt 2)) / 2; its tanh form
-// v (1 + tanh u) / 2, u = sqrt(2 / pi) (v + 0.044715 v^3), equals v / (1 + e^-2u), which
-// costs one exponential and one division like silu and has no cancellation for v < 0.
-template <int ACT>
-__device__ __forceinline__ float act_value(float v) {
-  if constexpr (ACT == kActRelu) return v < 0.f ? 0.f : v;
-  if constexpr (ACT == kActSilu) return __fdividef(v, 1.f + __expf(-v));
-  if constexpr (ACT == kActGelu) return 0.5f * v * (1.f + erff(v * 0.70710678f));
-  if constexpr (ACT == kActGeluTanh) {
-    const float m2u = v * fmaf(v * v, -0.071354816f, -1.5957691f);  // -2u
-    return __fdividef(v, 1.f + __expf(m2u));
-  }
-  return v;
+constexpr float kLog2e = 1.4426950408889634f;
+
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+  uint64_t d;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
+__device__ __forceinline__ uint64_t both(float v) { return f2pack(v, v); }
+
+// 1 / x to about one unit in the last place; 0 for an infinite x.
+__device__ __forceinline__ float rcp_approx(float x) {
+  float y;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
 }
 
-// Derivatives. relu'(0) = 0. silu' = s (1 + v (1 - s)); gelu' = Phi(v) + v phi(v); tanh
-// form with s = 1 / (1 + e^-2u): s + v s (1 - s) 2u'.
+// 1 / (1 + 2^t), elementwise: 0 where 2^t overflows.
+__device__ __forceinline__ uint64_t sigmoid_exp2(uint64_t t) {
+  float a, b;
+  f2unpack(t, a, b);
+  f2unpack(add2(f2pack(ex2_approx(a), ex2_approx(b)), both(1.f)), a, b);
+  return f2pack(rcp_approx(a), rcp_approx(b));
+}
+
+// Phi(-z sqrt 2) = erfc(z) / 2 for z = az / sqrt 2 >= 0 and e = exp(-z^2), by Abramowitz
+// and Stegun, Handbook of Mathematical Functions, 7.1.26:
+// erfc(z) = t (a1 + t (a2 + ... a5)) exp(-z^2) + err, t = 1 / (1 + 0.3275911 z),
+// |err| <= 1.5e-7 (here halved), below the rounding of every result that it enters.
+__device__ __forceinline__ uint64_t normal_tail(uint64_t az, uint64_t& e) {
+  const uint64_t d = fma2(az, both(0.3275911f * 0.70710678f), both(1.f));
+  const uint64_t x = mul2(mul2(az, az), both(-0.5f * kLog2e));
+  float a, b;
+  f2unpack(d, a, b);
+  const uint64_t t = f2pack(rcp_approx(a), rcp_approx(b));
+  f2unpack(x, a, b);
+  e = f2pack(ex2_approx(a), ex2_approx(b));
+  uint64_t q = fma2(t, both(0.5f * 1.061405429f), both(0.5f * -1.453152027f));
+  q = fma2(t, q, both(0.5f * 1.421413741f));
+  q = fma2(t, q, both(0.5f * -0.284496736f));
+  q = fma2(t, q, both(0.5f * 0.254829592f));
+  return mul2(mul2(t, q), e);
+}
+
+// relu(v) = max(v, 0) (a NaN stays one); silu(v) = v / (1 + e^-v); gelu(v) = v Phi(v) =
+// max(v, 0) - |v| Phi(-|v|), Phi the normal distribution (beyond |v| = 100 the second term
+// is 0); its tanh form v (1 + tanh u) / 2, u = sqrt(2 / pi) (v + 0.044715 v^3), equals
+// v / (1 + e^-2u), which costs no more than silu and has no cancellation for v < 0.
 template <int ACT>
-__device__ __forceinline__ float act_deriv(float v) {
-  if constexpr (ACT == kActRelu) return v <= 0.f ? 0.f : 1.f;
-  if constexpr (ACT == kActSilu) {
-    const float s = __fdividef(1.f, 1.f + __expf(-v));
-    return s * fmaf(v, 1.f - s, 1.f);
+__device__ __forceinline__ void act_pair(float& a, float& b) {
+  const uint64_t v = f2pack(a, b);
+  if constexpr (ACT == kActRelu) {
+    a = a < 0.f ? 0.f : a;
+    b = b < 0.f ? 0.f : b;
+  } else if constexpr (ACT == kActSilu) {
+    f2unpack(mul2(v, sigmoid_exp2(mul2(v, both(-kLog2e)))), a, b);
+  } else if constexpr (ACT == kActGeluTanh) {
+    const uint64_t p =
+        fma2(mul2(v, v), both(-0.071354816f * kLog2e), both(-1.5957691f * kLog2e));
+    f2unpack(mul2(v, sigmoid_exp2(mul2(v, p))), a, b);
+  } else if constexpr (ACT == kActGelu) {
+    uint64_t e;
+    const uint64_t az = f2pack(fminf(fabsf(a), 100.f), fminf(fabsf(b), 100.f));
+    const uint64_t neg = mul2(az, both(-1.f));
+    const uint64_t relu = f2pack(a < 0.f ? 0.f : a, b < 0.f ? 0.f : b);
+    f2unpack(fma2(neg, normal_tail(az, e), relu), a, b);
   }
-  if constexpr (ACT == kActGelu)
-    return fmaf(v * 0.39894228f, __expf(-0.5f * v * v), 0.5f * (1.f + erff(v * 0.70710678f)));
-  if constexpr (ACT == kActGeluTanh) {
-    const float q = v * v;
-    const float s = __fdividef(1.f, 1.f + __expf(v * fmaf(q, -0.071354816f, -1.5957691f)));
-    return fmaf(v * s * (1.f - s), fmaf(q, 0.21406445f, 1.5957691f), s);
+}
+
+// Derivatives. relu'(0) = 0. silu' = s (1 + v (1 - s)), s = 1 / (1 + e^-v); gelu' = Phi(v) +
+// v phi(v), Phi(v) = 1 - Phi(-v); tanh form with s = 1 / (1 + e^-2u): s + v s (1 - s) 2u'.
+template <int ACT>
+__device__ __forceinline__ void act_deriv_pair(float& a, float& b) {
+  const uint64_t v = f2pack(a, b), one = both(1.f), minus = both(-1.f);
+  if constexpr (ACT == kActRelu) {
+    a = a <= 0.f ? 0.f : 1.f;
+    b = b <= 0.f ? 0.f : 1.f;
+  } else if constexpr (ACT == kActSilu) {
+    const uint64_t s = sigmoid_exp2(mul2(v, both(-kLog2e)));
+    f2unpack(mul2(s, fma2(v, fma2(s, minus, one), one)), a, b);
+  } else if constexpr (ACT == kActGeluTanh) {
+    const uint64_t q = mul2(v, v);
+    const uint64_t p = fma2(q, both(-0.071354816f * kLog2e), both(-1.5957691f * kLog2e));
+    const uint64_t s = sigmoid_exp2(mul2(v, p));
+    const uint64_t du = fma2(q, both(0.21406445f), both(1.5957691f));
+    f2unpack(fma2(mul2(mul2(v, s), fma2(s, minus, one)), du, s), a, b);
+  } else if constexpr (ACT == kActGelu) {
+    uint64_t e;
+    const uint64_t t = normal_tail(f2pack(fminf(fabsf(a), 100.f), fminf(fabsf(b), 100.f)), e);
+    float ta, tb;
+    f2unpack(t, ta, tb);
+    const uint64_t cdf = f2pack(a < 0.f ? ta : 1.f - ta, b < 0.f ? tb : 1.f - tb);
+    f2unpack(fma2(mul2(v, both(0.39894228f)), e, cdf), a, b);
+  } else {
+    a = b = 1.f;
   }
-  return 1.f;
 }
 
 // f applied with the activation as a compile-time constant.
@@ -50,7 +117,7 @@ __device__ __forceinline__ void with_act(int act, F&& f) {
     case kActSilu: f(std::integral_constant<int, kActSilu>{}); break;
     case kActGelu: f(std::integral_constant<int, kActGelu>{}); break;
     case kActGeluTanh: f(std::integral_constant<int, kActGeluTanh>{}); break;
-    default: f(std::integral_constant<int, kActNone>{}); break;
+    default: break;
   }
 }
 
