@@ -89,7 +89,7 @@ int prepare(int* sms) {
   if (*sms > 0) return INFINI_OK;
   int n = 0;
   if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || n < 1 ||
-      linear_set_attributes() != cudaSuccess)
+      linear_set_attributes() != cudaSuccess || norm_set_attributes() != cudaSuccess)
     return INFINI_ERR_CUDA;
   *sms = n;
   g_sms[dev].store(n, std::memory_order_release);  // the same value from every thread

@@ -72,6 +72,7 @@ struct NormArgs {
 };
 
 constexpr int kMaxNormDim = 8192;
+cudaError_t norm_set_attributes();
 bool norm_vectorised(const NormArgs& a, bool f32);
 cudaError_t norm_forward_launch(const NormArgs& a, int kind, bool f32, int sms,
                                 cudaStream_t stream);

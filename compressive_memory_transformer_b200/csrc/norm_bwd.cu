@@ -9,183 +9,222 @@
 //   db = inv_b (g' - [mean g'] - bn mean(g' bn))
 //   dw_pre = sum dh rn, dc_pre = sum dh
 //
-// The statistics are formed again from x and b, which have to be read for dw_post and
-// dgate anyway. HBM-bound: x, b, dr, dh read once, dx, db written once. The sums over rows
-// stay in fp32 registers of the thread that holds the column, over all rows that its
-// worker takes; each block leaves one row of partial sums per vector, each chunk of a
-// gate group one row of dgate partials, and colsum / gate_sum add them in a fixed order.
+// The statistics are formed again from x and b, which have to be read for dw_post and dgate
+// anyway. HBM-bound: x, b, dr, dh read once, dx, db written once. A row's thread keeps the
+// sums over rows of its columns: of d bn and of d in registers, for as long as the gate row
+// stays the same (dgate = w sum d bn + c sum d; dw_post and dc_post get gate times the
+// sums), the others in shared memory: with them in registers the kernel spilled 0.5 to 1 KB
+// per thread. Each block leaves one row of partial sums per vector, each chunk of a gate
+// group one row of dgate, and colsum / gate_sum add them in a fixed order. The next row is
+// asked for in L2 while the present one is worked on.
 #include "norm_common.cuh"
 
 namespace infini {
 namespace {
 
+#ifndef NB_RES
+#define NB_RES 512
+#endif
+constexpr int kResident = NB_RES;  // threads per SM
+
+// Shared memory of a block's sums over rows.
+constexpr int acc_bytes(bool layer, int threads) {
+  return norm_sets(layer ? kNormLayer : kNormRms) * kP * threads * 8;
+}
+
+// The part of a norm's gradient that both norms share: with t the gradient of n(v) and vn =
+// n(v), t - [mean t] - vn mean(t vn), in place of t (to be multiplied by n's factor).
+template <bool LAYER, typename R>
+__device__ __forceinline__ void centre(Row16& t, const Row16& vn, float inv_d, R& red) {
+  uint64_t s1 = 0, s2 = 0;
+  INFINI_EACH_PAIR {
+    s1 = fma2(t.p[i], vn.p[i], s1);
+    if constexpr (LAYER) s2 = add2(s2, t.p[i]);
+  }
+  if constexpr (LAYER) {
+    const float2 m = red.sum2(halves(s1), halves(s2));
+    const uint64_t m1 = both(-m.x * inv_d), m2 = both(-m.y * inv_d);
+    INFINI_EACH_PAIR t.p[i] = add2(fma2(vn.p[i], m1, t.p[i]), m2);
+  } else {
+    const uint64_t m1 = both(-red.sum(halves(s1)) * inv_d);
+    INFINI_EACH_PAIR t.p[i] = fma2(vn.p[i], m1, t.p[i]);
+  }
+}
+
 template <typename T, int TPR, bool VEC, bool LAYER>
-__global__ void __launch_bounds__(norm_threads(TPR))
+__global__ void __launch_bounds__(norm_threads(TPR), kResident / norm_threads(TPR))
 norm_backward_kernel(const NormArgs a) {
   using L = RowLayout<T, TPR, VEC>;
   constexpr int kThreads = norm_threads(TPR), kWorkers = kThreads / TPR;
   constexpr int kSets = norm_sets(LAYER ? kNormLayer : kNormRms);
   __shared__ float2 sbuf[kWorkers][2][TPR / 32];
-  __shared__ float comb[kWorkers > 1 ? kThreads * kE : 1];
+  extern __shared__ uint64_t acc[];  // [set][pair][thread]
   const int w = threadIdx.x / TPR, t = threadIdx.x % TPR;
   RowSum<TPR> red{&sbuf[w], 1 + w};
   const int D = a.D;
   const float inv_d = 1.f / (float)D;
-  // 0: pre weight, 1: post weight, 2: pre bias, 3: post bias
-  float acc[kSets][kE] = {};
+  // sets: 0 dw_pre, 1 dw_post, 2 dc_pre, 3 dc_post
+  auto sum = [&](int set, int i) -> uint64_t& {
+    return acc[(set * kP + i) * kThreads + threadIdx.x];
+  };
+#pragma unroll
+  for (int s = 0; s < kSets; ++s)
+    INFINI_EACH_PAIR sum(s, i) = 0;
   const long long units = a.groups * a.cpg;
   for (long long u0 = (long long)blockIdx.x * kWorkers + w; u0 < units;
        u0 += (long long)gridDim.x * kWorkers) {
     const long long g = u0 / a.cpg, c = u0 % a.cpg;
     const long long r0 = g * a.group_rows + a.group_rows * c / a.cpg;
     const long long r1 = g * a.group_rows + a.group_rows * (c + 1) / a.cpg;
-    float ag[kE] = {};
+    Row16 pn, pd;  // sums over the unit's rows of d bn and of d
+    INFINI_EACH_PAIR pn.p[i] = pd.p[i] = 0;
     for (long long row = r0; row < r1; ++row) {
-      RowRaw<T, TPR, VEC> raw;
-      float q[kE], u[kE], bn[kE], v[kE], d[kE];
-      float inv_b = 1.f;
-      raw.load(a.x, row, D, t);
-      raw.get(v);
-#pragma unroll
-      for (int i = 0; i < kE; ++i) {
-        v[i] *= a.alpha;
-        d[i] = u[i] = bn[i] = 0.f;
+      RowRaw<T, TPR, VEC> rx, rb, rr, rh;
+      rx.load(a.x, row, D, t);
+      if (a.b) rb.load(a.b, row, D, t);
+      // dh, and dr later, when registers are free again (fp32: both later)
+      if (sizeof(T) == 2 && a.dh) rh.load(a.dh, row, D, t);
+      if (VEC && t == 0 && row + 1 < r1) {
+        prefetch_row<T>(a.x, row + 1, D);
+        if (a.b) prefetch_row<T>(a.b, row + 1, D);
+        if (a.dh) prefetch_row<T>(a.dh, row + 1, D);
+        if (a.dr) prefetch_row<T>(a.dr, row + 1, D);
       }
+      Row16 v = rx.get(), bn;
+      float inv_b = 1.f;
+      INFINI_EACH_PAIR v.p[i] = mul2(v.p[i], both(a.alpha));
       if (a.b) {
-        raw.load(a.b, row, D, t);
-        raw.get(bn);
+        bn = rb.get();
+        Row16 u = bn;
         if (a.post_w) {
           inv_b = normalise<L, LAYER>(bn, t, D, inv_d, a.eps, red);
-          load_param<L, VEC>(a.post_w, D, t, q);
-#pragma unroll
-          for (int i = 0; i < kE; ++i) u[i] = bn[i] * q[i];
-          if (a.post_b) {
-            load_param<L, VEC>(a.post_b, D, t, q);
-#pragma unroll
-            for (int i = 0; i < kE; ++i) u[i] += q[i];
+          const Row16 q = load_param<L>(a.post_w, D, t);
+          if (LAYER && a.post_b) {
+            const Row16 k = load_param<L>(a.post_b, D, t);
+            INFINI_EACH_PAIR u.p[i] = fma2(bn.p[i], q.p[i], k.p[i]);
+          } else {
+            INFINI_EACH_PAIR u.p[i] = mul2(bn.p[i], q.p[i]);
           }
-        } else {
-#pragma unroll
-          for (int i = 0; i < kE; ++i) u[i] = bn[i];
         }
         if (a.gate) {
-          load_param<L, VEC>(a.gate + g * D, D, t, q);
-#pragma unroll
-          for (int i = 0; i < kE; ++i) v[i] = fmaf(q[i], u[i], v[i]);
+          const Row16 q = load_param<L>(a.gate + g * D, D, t);
+          INFINI_EACH_PAIR v.p[i] = fma2(q.p[i], u.p[i], v.p[i]);
         } else {
-#pragma unroll
-          for (int i = 0; i < kE; ++i) v[i] += u[i];
+          INFINI_EACH_PAIR v.p[i] = add2(u.p[i], v.p[i]);
         }
+      }
+      if (a.dr) rr.load(a.dr, row, D, t);
+      Row16 d;
+      INFINI_EACH_PAIR d.p[i] = 0;
+      if (a.dh) {
+        if (sizeof(T) == 4) rh.load(a.dh, row, D, t);
+        const uint64_t inv_r = both(normalise<L, LAYER>(v, t, D, inv_d, a.eps, red));
+        Row16 h = rh.get();
+        const Row16 q = load_param<L>(a.pre_w, D, t);
+        INFINI_EACH_PAIR {
+          sum(0, i) = fma2(h.p[i], v.p[i], sum(0, i));
+          if constexpr (LAYER) sum(2, i) = add2(sum(2, i), h.p[i]);
+          h.p[i] = mul2(h.p[i], q.p[i]);
+        }
+        centre<LAYER>(h, v, inv_d, red);
+        INFINI_EACH_PAIR d.p[i] = mul2(h.p[i], inv_r);
       }
       if (a.dr) {
-        raw.load(a.dr, row, D, t);
-        raw.get(d);
-      }
-      if (a.dh) {
-        float p[kE];
-        const float inv_r = normalise<L, LAYER>(v, t, D, inv_d, a.eps, red);
-        raw.load(a.dh, row, D, t);
-        raw.get(p);
-        load_param<L, VEC>(a.pre_w, D, t, q);
-        float s1 = 0.f, s2 = 0.f;
-#pragma unroll
-        for (int i = 0; i < kE; ++i) {
-          acc[0][i] = fmaf(p[i], v[i], acc[0][i]);
-          if constexpr (LAYER) acc[2][i] += p[i];
-          p[i] *= q[i];
-          s1 = fmaf(p[i], v[i], s1);
-          s2 += p[i];
-        }
-        const float2 m = red.sum2(s1, s2);
-        const float m1 = m.x * inv_d, m2 = LAYER ? m.y * inv_d : 0.f;
-#pragma unroll
-        for (int i = 0; i < kE; ++i)
-          if (inside<L>(t, i, D)) d[i] = fmaf(inv_r, p[i] - m2 - v[i] * m1, d[i]);
+        const Row16 k = rr.get();
+        INFINI_EACH_PAIR d.p[i] = add2(d.p[i], k.p[i]);
       }
       if (a.dx) {
-#pragma unroll
-        for (int i = 0; i < kE; ++i) v[i] = a.alpha * d[i];
+        INFINI_EACH_PAIR v.p[i] = mul2(d.p[i], both(a.alpha));
         store_row<T, TPR, VEC>(a.dx, row, D, t, v);
       }
       if (!a.b) continue;
+      INFINI_EACH_PAIR {
+        pn.p[i] = fma2(d.p[i], bn.p[i], pn.p[i]);
+        if constexpr (LAYER) pd.p[i] = add2(pd.p[i], d.p[i]);
+      }
       if (a.gate) {
-        load_param<L, VEC>(a.gate + g * D, D, t, q);
-#pragma unroll
-        for (int i = 0; i < kE; ++i) {
-          ag[i] = fmaf(d[i], u[i], ag[i]);
-          d[i] *= q[i];
-        }
+        const Row16 q = load_param<L>(a.gate + g * D, D, t);
+        INFINI_EACH_PAIR d.p[i] = mul2(d.p[i], q.p[i]);
       }
       if (a.post_w) {
-        load_param<L, VEC>(a.post_w, D, t, q);
-        float s1 = 0.f, s2 = 0.f;
-#pragma unroll
-        for (int i = 0; i < kE; ++i) {
-          acc[1][i] = fmaf(d[i], bn[i], acc[1][i]);
-          if constexpr (LAYER) acc[3][i] += d[i];
-          d[i] *= q[i];
-          s1 = fmaf(d[i], bn[i], s1);
-          s2 += d[i];
-        }
-        const float2 m = red.sum2(s1, s2);
-        const float m1 = m.x * inv_d, m2 = LAYER ? m.y * inv_d : 0.f;
-#pragma unroll
-        for (int i = 0; i < kE; ++i) d[i] = inv_b * (d[i] - m2 - bn[i] * m1);
+        const Row16 q = load_param<L>(a.post_w, D, t);
+        INFINI_EACH_PAIR d.p[i] = mul2(d.p[i], q.p[i]);
+        centre<LAYER>(d, bn, inv_d, red);
+        INFINI_EACH_PAIR d.p[i] = mul2(d.p[i], both(inv_b));
       }
       if (a.db) store_row<T, TPR, VEC>(a.db, row, D, t, d);
     }
+    // the unit's rows share a gate row
+    if (a.post_w) {
+      Row16 e = pn, f = pd;
+      if (a.gate) {
+        const Row16 q = load_param<L>(a.gate + g * D, D, t);
+        INFINI_EACH_PAIR {
+          e.p[i] = mul2(e.p[i], q.p[i]);
+          if constexpr (LAYER) f.p[i] = mul2(f.p[i], q.p[i]);
+        }
+      }
+      INFINI_EACH_PAIR {
+        sum(1, i) = add2(sum(1, i), e.p[i]);
+        if constexpr (LAYER) sum(3, i) = add2(sum(3, i), f.p[i]);
+      }
+    }
     if (a.gpart) {
-#pragma unroll
-      for (int i = 0; i < kE; ++i)
-        if (inside<L>(t, i, D))
-          a.gpart[u0 * D + L::col(t, i / L::kPiece) + i % L::kPiece] = ag[i];
+      if (a.post_w) {
+        const Row16 q = load_param<L>(a.post_w, D, t);
+        INFINI_EACH_PAIR pn.p[i] = mul2(pn.p[i], q.p[i]);
+        if (LAYER && a.post_b) {
+          const Row16 k = load_param<L>(a.post_b, D, t);
+          INFINI_EACH_PAIR pn.p[i] = fma2(pd.p[i], k.p[i], pn.p[i]);
+        }
+      }
+      float* dst = a.gpart + u0 * D;
+      INFINI_EACH_PAIR {
+        if (L::col(t, 2 * i) < D) dst[L::col(t, 2 * i)] = lo_of(pn.p[i]);
+        if (L::col(t, 2 * i + 1) < D) dst[L::col(t, 2 * i + 1)] = hi_of(pn.p[i]);
+      }
     }
   }
   if (!a.part) return;
+  __syncthreads();
+  if (w != 0) return;
 #pragma unroll
   for (int s = 0; s < kSets; ++s) {
     float* dst = a.part + ((long long)blockIdx.x * kSets + s) * D;
-    if constexpr (kWorkers > 1) {
-      __syncthreads();
+    INFINI_EACH_PAIR {
+      uint64_t v = sum(s, i);
 #pragma unroll
-      for (int i = 0; i < kE; ++i) comb[i * kThreads + threadIdx.x] = acc[s][i];
-      __syncthreads();
-      if (w == 0) {
-#pragma unroll
-        for (int i = 0; i < kE; ++i) {
-          float v = acc[s][i];
-#pragma unroll
-          for (int k = 1; k < kWorkers; ++k) v += comb[i * kThreads + k * TPR + t];
-          if (inside<L>(t, i, D)) dst[L::col(t, i / L::kPiece) + i % L::kPiece] = v;
-        }
-      }
-    } else {
-#pragma unroll
-      for (int i = 0; i < kE; ++i)
-        if (inside<L>(t, i, D)) dst[L::col(t, i / L::kPiece) + i % L::kPiece] = acc[s][i];
+      for (int k = 1; k < kWorkers; ++k)
+        v = add2(v, acc[(s * kP + i) * kThreads + k * TPR + t]);
+      if (L::col(t, 2 * i) < D) dst[L::col(t, 2 * i)] = lo_of(v);
+      if (L::col(t, 2 * i + 1) < D) dst[L::col(t, 2 * i + 1)] = hi_of(v);
     }
   }
 }
 
-template <typename T, int TPR, bool VEC>
-cudaError_t launch(const NormArgs& a, int kind, int blocks, cudaStream_t stream) {
-  constexpr int kThreads = norm_threads(TPR);
-  if (kind == kNormLayer)
-    norm_backward_kernel<T, TPR, VEC, true><<<blocks, kThreads, 0, stream>>>(a);
-  else
-    norm_backward_kernel<T, TPR, VEC, false><<<blocks, kThreads, 0, stream>>>(a);
-  return cudaGetLastError();
+template <typename T, bool VEC, bool LAYER>
+cudaError_t launch(const NormArgs& a, int blocks, cudaStream_t stream) {
+  return with_tpr(a.D, [&](auto tpr) {
+    constexpr int TPR = decltype(tpr)::value, kThreads = norm_threads(TPR);
+    norm_backward_kernel<T, TPR, VEC, LAYER>
+        <<<blocks, kThreads, acc_bytes(LAYER, kThreads), stream>>>(a);
+    return cudaGetLastError();
+  });
 }
 
-template <typename T, bool VEC>
-cudaError_t by_width(const NormArgs& a, int kind, int blocks, cudaStream_t stream) {
-  switch (norm_tpr(a.D)) {
-    case 32: return launch<T, 32, VEC>(a, kind, blocks, stream);
-    case 128: return launch<T, 128, VEC>(a, kind, blocks, stream);
-    case 256: return launch<T, 256, VEC>(a, kind, blocks, stream);
-    case 512: return launch<T, 512, VEC>(a, kind, blocks, stream);
-    default: return launch<T, 1024, VEC>(a, kind, blocks, stream);
+template <typename T, bool VEC, bool LAYER>
+cudaError_t allow() {
+  cudaError_t e = cudaSuccess;
+  for (int d : {512, 1024, 2048, 4096, 8192}) {  // one width of each number of threads
+    const cudaError_t f = with_tpr(d, [](auto tpr) {
+      constexpr int TPR = decltype(tpr)::value;
+      return cudaFuncSetAttribute(norm_backward_kernel<T, TPR, VEC, LAYER>,
+                                  cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                  acc_bytes(LAYER, norm_threads(TPR)));
+    });
+    if (e == cudaSuccess) e = f;
   }
+  return e;
 }
 
 __global__ void __launch_bounds__(256)
@@ -212,7 +251,7 @@ gate_sum_kernel(const float* __restrict__ gpart, float* __restrict__ dgate, long
 void norm_backward_plan(long long rows, int D, long long groups, int sms, int* blocks,
                         long long* cpg) {
   const int threads = norm_threads(norm_tpr(D)), workers = threads / norm_tpr(D);
-  const long long per_sm = 1024 / threads;
+  const long long per_sm = kResident / threads;
   long long nb = (rows + workers - 1) / workers;
   if (nb > per_sm * sms) nb = per_sm * sms;
   *blocks = (int)(nb < 1 ? 1 : nb);
@@ -222,13 +261,31 @@ void norm_backward_plan(long long rows, int D, long long groups, int sms, int* b
   *cpg = c < 1 ? 1 : c;
 }
 
+cudaError_t norm_set_attributes() {
+  cudaError_t e = allow<__nv_bfloat16, true, false>();
+  if (e == cudaSuccess) e = allow<__nv_bfloat16, true, true>();
+  if (e == cudaSuccess) e = allow<__nv_bfloat16, false, false>();
+  if (e == cudaSuccess) e = allow<__nv_bfloat16, false, true>();
+  if (e == cudaSuccess) e = allow<float, true, false>();
+  if (e == cudaSuccess) e = allow<float, true, true>();
+  if (e == cudaSuccess) e = allow<float, false, false>();
+  if (e == cudaSuccess) e = allow<float, false, true>();
+  return e;
+}
+
 cudaError_t norm_backward_launch(const NormArgs& a, int kind, bool f32, int blocks,
                                  cudaStream_t stream) {
-  if (norm_vectorised(a, f32))
-    return f32 ? by_width<float, true>(a, kind, blocks, stream)
-               : by_width<__nv_bfloat16, true>(a, kind, blocks, stream);
-  return f32 ? by_width<float, false>(a, kind, blocks, stream)
-             : by_width<__nv_bfloat16, false>(a, kind, blocks, stream);
+  const bool vec = norm_vectorised(a, f32);
+  if (kind == kNormLayer) {
+    if (f32) return vec ? launch<float, true, true>(a, blocks, stream)
+                        : launch<float, false, true>(a, blocks, stream);
+    return vec ? launch<__nv_bfloat16, true, true>(a, blocks, stream)
+               : launch<__nv_bfloat16, false, true>(a, blocks, stream);
+  }
+  if (f32) return vec ? launch<float, true, false>(a, blocks, stream)
+                      : launch<float, false, false>(a, blocks, stream);
+  return vec ? launch<__nv_bfloat16, true, false>(a, blocks, stream)
+             : launch<__nv_bfloat16, false, false>(a, blocks, stream);
 }
 
 cudaError_t gate_sum_launch(const float* gpart, float* dgate, long long groups, long long cpg,

@@ -1,40 +1,55 @@
 // norm_common.cuh — what the norm kernels share: the layout of a row over its threads,
 // loads and stores, and sums over a row's threads.
 //
-// A row of D elements belongs to TPR threads of a block (a "worker"); each thread holds 8
-// elements in fp32 registers. Vector layout (16-byte pieces): bf16, thread t has elements
-// [8t, 8t + 8); fp32, [4t, 4t + 4) and [4 TPR + 4t, + 4), so that neighbouring threads
-// read neighbouring 16-byte pieces. Scalar layout, for odd widths and rows that do not
-// start on 16 bytes: element t + i TPR for i = 0..7.
+// A row of D elements belongs to TPR threads of a block (a "worker"); each thread holds 16
+// elements as 8 fp32 pairs, on which the arithmetic is packed (f32x2). Vector layout
+// (16-byte pieces): piece j of thread t is the (t + j TPR)-th of the row, so that
+// neighbouring threads read neighbouring pieces; 8 elements each of bf16, 4 of fp32. Scalar
+// layout, for odd widths and rows that do not start on 16 bytes: element t + i TPR for
+// i = 0..15. Elements outside the row are held as 0.
 #pragma once
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 #include <cstdint>
+#include <type_traits>
 
 #include "block_ops.h"
 #include "sm100.cuh"
 
 namespace infini {
 
-constexpr int kE = 8;  // elements of a row per thread
+constexpr int kE = 16;      // elements of a row per thread
+constexpr int kP = kE / 2;  // pairs
+
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+  uint64_t d;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
+__device__ __forceinline__ uint64_t both(float v) { return f2pack(v, v); }
+__device__ __forceinline__ float lo_of(uint64_t v) { return __uint_as_float((uint32_t)v); }
+__device__ __forceinline__ float hi_of(uint64_t v) { return __uint_as_float((uint32_t)(v >> 32)); }
+
+struct Row16 {
+  uint64_t p[kP];
+};
+#define INFINI_EACH_PAIR _Pragma("unroll") for (int i = 0; i < kP; ++i)
 
 template <typename T, int TPR, bool VEC>
 struct RowLayout {
-  static constexpr bool kF32 = sizeof(T) == 4;
-  // First element of piece j of thread t (VEC) and the pieces' length.
-  static constexpr int kPieces = VEC ? (kF32 ? 2 : 1) : kE;
-  static constexpr int kPiece = kE / kPieces;
-  __device__ static __forceinline__ int col(int t, int j) {
-    if constexpr (VEC) return kF32 ? 4 * t + 4 * TPR * j : 8 * t;
-    return t + TPR * j;
+  static constexpr int kPiece = VEC ? 16 / (int)sizeof(T) : 1;  // elements of a piece
+  static constexpr int kPieces = kE / kPiece;
+  // Column of element e of thread t.
+  __device__ static __forceinline__ int col(int t, int e) {
+    return kPiece * (t + TPR * (e / kPiece)) + e % kPiece;
   }
 };
 
-// One row's elements of one thread as loaded (16 bytes of bf16, 32 of fp32).
+// One row's elements of one thread as loaded (32 bytes of bf16, 64 of fp32).
 template <typename T, int TPR, bool VEC>
 struct RowRaw {
   using L = RowLayout<T, TPR, VEC>;
-  uint32_t w[sizeof(T) == 2 ? 4 : 8];
+  uint32_t w[kE * sizeof(T) / 4];
 
   __device__ __forceinline__ void load(const void* base, long long row, int D, int t) {
     const T* p = static_cast<const T*>(base) + row * D;
@@ -42,7 +57,8 @@ struct RowRaw {
 #pragma unroll
       for (int j = 0; j < L::kPieces; ++j) {
         uint4 v = make_uint4(0, 0, 0, 0);
-        if (L::col(t, j) < D) v = __ldcs(reinterpret_cast<const uint4*>(p + L::col(t, j)));
+        const int c = L::col(t, j * L::kPiece);
+        if (c < D) v = __ldcs(reinterpret_cast<const uint4*>(p + c));
         w[4 * j] = v.x; w[4 * j + 1] = v.y; w[4 * j + 2] = v.z; w[4 * j + 3] = v.w;
       }
     } else if constexpr (sizeof(T) == 4) {
@@ -50,82 +66,79 @@ struct RowRaw {
       for (int i = 0; i < kE; ++i)
         w[i] = L::col(t, i) < D ? reinterpret_cast<const uint32_t*>(p)[L::col(t, i)] : 0u;
     } else {
+      const uint16_t* q = reinterpret_cast<const uint16_t*>(p);
 #pragma unroll
       for (int i = 0; i < kE; i += 2) {
-        const uint16_t* q = reinterpret_cast<const uint16_t*>(p);
         const uint32_t lo = L::col(t, i) < D ? q[L::col(t, i)] : 0u;
         const uint32_t hi = L::col(t, i + 1) < D ? q[L::col(t, i + 1)] : 0u;
         w[i / 2] = lo | (hi << 16);
       }
     }
   }
-  __device__ __forceinline__ void get(float (&v)[kE]) const {
-    if constexpr (sizeof(T) == 4) {
-#pragma unroll
-      for (int i = 0; i < kE; ++i) v[i] = __uint_as_float(w[i]);
-    } else {
-#pragma unroll
-      for (int i = 0; i < kE / 2; ++i) {
-        v[2 * i] = __uint_as_float(w[i] << 16);
-        v[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
-      }
+  __device__ __forceinline__ Row16 get() const {
+    Row16 r;
+    INFINI_EACH_PAIR {
+      if constexpr (sizeof(T) == 4)
+        r.p[i] = (uint64_t)w[2 * i] | ((uint64_t)w[2 * i + 1] << 32);
+      else
+        r.p[i] = f2pack(__uint_as_float(w[i] << 16), __uint_as_float(w[i] & 0xffff0000u));
     }
+    return r;
   }
 };
 
-// Whether element i of thread t lies inside a row.
-template <typename L>
-__device__ __forceinline__ bool inside(int t, int i, int D) {
-  return L::col(t, i / L::kPiece) < D;
-}
-
 template <typename T, int TPR, bool VEC>
 __device__ __forceinline__ void store_row(void* base, long long row, int D, int t,
-                                          const float (&v)[kE]) {
+                                          const Row16& v) {
   using L = RowLayout<T, TPR, VEC>;
   T* p = static_cast<T*>(base) + row * D;
-  if constexpr (VEC && sizeof(T) == 2) {
-    if (L::col(t, 0) < D)
-      *reinterpret_cast<uint4*>(p + L::col(t, 0)) =
-          make_uint4(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]), pack_bf16x2(v[4], v[5]),
-                     pack_bf16x2(v[6], v[7]));
-  } else if constexpr (VEC) {
-#pragma unroll
-    for (int j = 0; j < 2; ++j)
-      if (L::col(t, j) < D)
-        *reinterpret_cast<float4*>(p + L::col(t, j)) =
-            make_float4(v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]);
-  } else {
-#pragma unroll
-    for (int i = 0; i < kE; ++i)
-      if (L::col(t, i) < D) {
-        if constexpr (sizeof(T) == 2)
-          p[L::col(t, i)] = __float2bfloat16(v[i]);
-        else
-          p[L::col(t, i)] = v[i];
-      }
-  }
-}
-
-// A vector of fp32 parameters in the row's layout (`fill` outside the row).
-template <typename L, bool VEC>
-__device__ __forceinline__ void load_param(const float* p, int D, int t, float (&v)[kE]) {
-#pragma unroll
-  for (int i = 0; i < kE; ++i) v[i] = 0.f;
   if constexpr (VEC) {
 #pragma unroll
-    for (int i = 0; i < kE; i += 4) {
-      const int c = L::col(t, i / L::kPiece) + i % L::kPiece;
-      if (c < D) {
-        const float4 f = __ldg(reinterpret_cast<const float4*>(p + c));
-        v[i] = f.x; v[i + 1] = f.y; v[i + 2] = f.z; v[i + 3] = f.w;
-      }
+    for (int j = 0; j < L::kPieces; ++j) {
+      const int c = L::col(t, j * L::kPiece);
+      if (c >= D) continue;
+      uint4 o;
+      if constexpr (sizeof(T) == 2)
+        o = make_uint4(pack_bf16x2(lo_of(v.p[4 * j]), hi_of(v.p[4 * j])),
+                       pack_bf16x2(lo_of(v.p[4 * j + 1]), hi_of(v.p[4 * j + 1])),
+                       pack_bf16x2(lo_of(v.p[4 * j + 2]), hi_of(v.p[4 * j + 2])),
+                       pack_bf16x2(lo_of(v.p[4 * j + 3]), hi_of(v.p[4 * j + 3])));
+      else
+        o = make_uint4((uint32_t)v.p[2 * j], (uint32_t)(v.p[2 * j] >> 32),
+                       (uint32_t)v.p[2 * j + 1], (uint32_t)(v.p[2 * j + 1] >> 32));
+      *reinterpret_cast<uint4*>(p + c) = o;
     }
   } else {
 #pragma unroll
-    for (int i = 0; i < kE; ++i)
-      if (L::col(t, i) < D) v[i] = __ldg(p + L::col(t, i));
+    for (int e = 0; e < kE; ++e)
+      if (L::col(t, e) < D) {
+        const float f = e % 2 ? hi_of(v.p[e / 2]) : lo_of(v.p[e / 2]);
+        if constexpr (sizeof(T) == 2)
+          p[L::col(t, e)] = __float2bfloat16(f);
+        else
+          p[L::col(t, e)] = f;
+      }
   }
+}
+
+// A vector of fp32 parameters in the row's layout.
+template <typename L>
+__device__ __forceinline__ Row16 load_param(const float* p, int D, int t) {
+  Row16 r;
+  if constexpr (L::kPiece > 1) {
+#pragma unroll
+    for (int e = 0; e < kE; e += 4) {
+      const int c = L::col(t, e);
+      float4 f = make_float4(0.f, 0.f, 0.f, 0.f);
+      if (c < D) f = __ldg(reinterpret_cast<const float4*>(p + c));
+      r.p[e / 2] = f2pack(f.x, f.y);
+      r.p[e / 2 + 1] = f2pack(f.z, f.w);
+    }
+  } else {
+    INFINI_EACH_PAIR r.p[i] = f2pack(L::col(t, 2 * i) < D ? __ldg(p + L::col(t, 2 * i)) : 0.f,
+                                     L::col(t, 2 * i + 1) < D ? __ldg(p + L::col(t, 2 * i + 1)) : 0.f);
+  }
+  return r;
 }
 
 // Sums over the TPR threads of a row, the same in every thread and in a fixed order
@@ -160,35 +173,73 @@ struct RowSum {
     }
     return make_float2(a, b);
   }
-  __device__ __forceinline__ float sum(float a) { return sum2(a, 0.f).x; }
+  __device__ __forceinline__ float sum(float a) {
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) a += __shfl_xor_sync(0xffffffffu, a, o);
+    if constexpr (kWarps > 1) {
+      const int w = (threadIdx.x % TPR) >> 5;
+      if ((threadIdx.x & 31) == 0) (*buf)[flip][w].x = a;
+      named_bar_sync((uint32_t)bar, TPR);
+      a = 0.f;
+#pragma unroll
+      for (int i = 0; i < kWarps; ++i) a += (*buf)[flip][i].x;
+      flip ^= 1;
+    }
+    return a;
+  }
 };
 
-// v -> (v - mean) / sd or v / rms; elements outside the row become 0. The variance is the
+// The sum of the two halves of a pair.
+__device__ __forceinline__ float halves(uint64_t v) { return lo_of(v) + hi_of(v); }
+
+// v -> (v - mean) / sd or v / rms; elements outside the row stay 0. The variance is the
 // mean of the squared distances from the mean (a second sum), never E v^2 - mean^2.
 template <typename L, bool LAYER, typename R>
-__device__ __forceinline__ float normalise(float (&v)[kE], int t, int D, float inv_d, float eps,
+__device__ __forceinline__ float normalise(Row16& v, int t, int D, float inv_d, float eps,
                                            R& red) {
-  float s = 0.f;
   if constexpr (LAYER) {
+    uint64_t s = v.p[0];
 #pragma unroll
-    for (int i = 0; i < kE; ++i) s += v[i];
-    const float mean = red.sum(s) * inv_d;
-#pragma unroll
-    for (int i = 0; i < kE; ++i) v[i] = inside<L>(t, i, D) ? v[i] - mean : 0.f;
-    s = 0.f;
+    for (int i = 1; i < kP; ++i) s = add2(s, v.p[i]);
+    const float mean = red.sum(halves(s)) * inv_d;
+    INFINI_EACH_PAIR {
+      const uint64_t c = add2(v.p[i], both(-mean));
+      v.p[i] = f2pack(L::col(t, 2 * i) < D ? lo_of(c) : 0.f,
+                      L::col(t, 2 * i + 1) < D ? hi_of(c) : 0.f);
+    }
   }
-#pragma unroll
-  for (int i = 0; i < kE; ++i) s = fmaf(v[i], v[i], s);
-  const float inv = 1.f / sqrtf(fmaf(red.sum(s), inv_d, eps));
-#pragma unroll
-  for (int i = 0; i < kE; ++i) v[i] *= inv;
+  uint64_t s = 0;
+  INFINI_EACH_PAIR s = fma2(v.p[i], v.p[i], s);
+  const float inv = rsqrtf(fmaf(red.sum(halves(s)), inv_d, eps));
+  INFINI_EACH_PAIR v.p[i] = mul2(v.p[i], both(inv));
   return inv;
+}
+
+// Asks for a row's bytes in L2 ahead of their loads (rows on 16 bytes only).
+template <typename T>
+__device__ __forceinline__ void prefetch_row(const void* base, long long row, int D) {
+  asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(static_cast<const T*>(base) +
+                                                                  row * D),
+               "r"((uint32_t)(D * sizeof(T)))
+               : "memory");
 }
 
 // Threads per row for a width, and threads per block.
 constexpr int norm_tpr(int D) {
-  return D <= 256 ? 32 : D <= 1024 ? 128 : D <= 2048 ? 256 : D <= 4096 ? 512 : 1024;
+  return D <= 512 ? 32 : D <= 1024 ? 64 : D <= 2048 ? 128 : D <= 4096 ? 256 : 512;
 }
 constexpr int norm_threads(int tpr) { return tpr < 256 ? 256 : tpr; }
+
+// f(threads per row) for a width.
+template <typename F>
+cudaError_t with_tpr(int D, F&& f) {
+  switch (norm_tpr(D)) {
+    case 32: return f(std::integral_constant<int, 32>{});
+    case 64: return f(std::integral_constant<int, 64>{});
+    case 128: return f(std::integral_constant<int, 128>{});
+    case 256: return f(std::integral_constant<int, 256>{});
+    default: return f(std::integral_constant<int, 512>{});
+  }
+}
 
 }  // namespace infini

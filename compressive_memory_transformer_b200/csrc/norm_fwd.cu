@@ -14,8 +14,13 @@
 namespace infini {
 namespace {
 
+#ifndef NF_RES
+#define NF_RES 512
+#endif
+constexpr int kResident = NF_RES;  // threads per SM
+
 template <typename T, int TPR, bool VEC, bool LAYER>
-__global__ void __launch_bounds__(norm_threads(TPR))
+__global__ void __launch_bounds__(norm_threads(TPR), kResident / norm_threads(TPR))
 norm_forward_kernel(const NormArgs a) {
   using L = RowLayout<T, TPR, VEC>;
   constexpr int kWorkers = norm_threads(TPR) / TPR;
@@ -32,76 +37,62 @@ norm_forward_kernel(const NormArgs a) {
     if (a.b) nb.load(a.b, row, D, t);
   }
   for (; row < a.rows; row += step) {
-    float v[kE], q[kE];
-    nx.get(v);
-#pragma unroll
-    for (int i = 0; i < kE; ++i) v[i] *= a.alpha;
+    Row16 v = nx.get();
+    INFINI_EACH_PAIR v.p[i] = mul2(v.p[i], both(a.alpha));
     if (a.b) {
-      float u[kE];
-      nb.get(u);
+      Row16 u = nb.get();
       if (row + step < a.rows) {
         nx.load(a.x, row + step, D, t);
         nb.load(a.b, row + step, D, t);
       }
       if (a.post_w) {
         normalise<L, LAYER>(u, t, D, inv_d, a.eps, red);
-        load_param<L, VEC>(a.post_w, D, t, q);
-#pragma unroll
-        for (int i = 0; i < kE; ++i) u[i] *= q[i];
+        const Row16 q = load_param<L>(a.post_w, D, t);
         if (a.post_b) {
-          load_param<L, VEC>(a.post_b, D, t, q);
-#pragma unroll
-          for (int i = 0; i < kE; ++i) u[i] += q[i];
+          const Row16 c = load_param<L>(a.post_b, D, t);
+          INFINI_EACH_PAIR u.p[i] = fma2(u.p[i], q.p[i], c.p[i]);
+        } else {
+          INFINI_EACH_PAIR u.p[i] = mul2(u.p[i], q.p[i]);
         }
       }
       if (a.gate) {
-        load_param<L, VEC>(a.gate + (row / a.group_rows) * D, D, t, q);
-#pragma unroll
-        for (int i = 0; i < kE; ++i) u[i] *= q[i];
+        const Row16 q = load_param<L>(a.gate + (row / a.group_rows) * D, D, t);
+        INFINI_EACH_PAIR v.p[i] = fma2(u.p[i], q.p[i], v.p[i]);
+      } else {
+        INFINI_EACH_PAIR v.p[i] = add2(u.p[i], v.p[i]);
       }
-#pragma unroll
-      for (int i = 0; i < kE; ++i) v[i] += u[i];
     } else if (row + step < a.rows) {
       nx.load(a.x, row + step, D, t);
     }
     if (a.r) store_row<T, TPR, VEC>(a.r, row, D, t, v);
     if (a.h) {
       normalise<L, LAYER>(v, t, D, inv_d, a.eps, red);
-      load_param<L, VEC>(a.pre_w, D, t, q);
-#pragma unroll
-      for (int i = 0; i < kE; ++i) v[i] *= q[i];
+      const Row16 q = load_param<L>(a.pre_w, D, t);
       if (a.pre_b) {
-        load_param<L, VEC>(a.pre_b, D, t, q);
-#pragma unroll
-        for (int i = 0; i < kE; ++i) v[i] += q[i];
+        const Row16 c = load_param<L>(a.pre_b, D, t);
+        INFINI_EACH_PAIR v.p[i] = fma2(v.p[i], q.p[i], c.p[i]);
+      } else {
+        INFINI_EACH_PAIR v.p[i] = mul2(v.p[i], q.p[i]);
       }
       store_row<T, TPR, VEC>(a.h, row, D, t, v);
     }
   }
 }
 
-template <typename T, int TPR, bool VEC>
-cudaError_t launch(const NormArgs& a, int kind, int sms, cudaStream_t stream) {
-  constexpr int kThreads = norm_threads(TPR), kWorkers = kThreads / TPR;
-  const long long need = (a.rows + kWorkers - 1) / kWorkers;
-  const long long most = (long long)sms * (2048 / kThreads);
-  const unsigned grid = (unsigned)(need < most ? need : most);
-  if (kind == kNormLayer)
-    norm_forward_kernel<T, TPR, VEC, true><<<grid, kThreads, 0, stream>>>(a);
-  else
-    norm_forward_kernel<T, TPR, VEC, false><<<grid, kThreads, 0, stream>>>(a);
-  return cudaGetLastError();
-}
-
 template <typename T, bool VEC>
-cudaError_t by_width(const NormArgs& a, int kind, int sms, cudaStream_t stream) {
-  switch (norm_tpr(a.D)) {
-    case 32: return launch<T, 32, VEC>(a, kind, sms, stream);
-    case 128: return launch<T, 128, VEC>(a, kind, sms, stream);
-    case 256: return launch<T, 256, VEC>(a, kind, sms, stream);
-    case 512: return launch<T, 512, VEC>(a, kind, sms, stream);
-    default: return launch<T, 1024, VEC>(a, kind, sms, stream);
-  }
+cudaError_t launch(const NormArgs& a, int kind, int sms, cudaStream_t stream) {
+  return with_tpr(a.D, [&](auto tpr) {
+    constexpr int TPR = decltype(tpr)::value;
+    constexpr int kThreads = norm_threads(TPR), kWorkers = kThreads / TPR;
+    const long long need = (a.rows + kWorkers - 1) / kWorkers;
+    const long long most = (long long)sms * (kResident / kThreads);
+    const unsigned grid = (unsigned)(need < most ? need : most);
+    if (kind == kNormLayer)
+      norm_forward_kernel<T, TPR, VEC, true><<<grid, kThreads, 0, stream>>>(a);
+    else
+      norm_forward_kernel<T, TPR, VEC, false><<<grid, kThreads, 0, stream>>>(a);
+    return cudaGetLastError();
+  });
 }
 
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
@@ -119,10 +110,10 @@ bool norm_vectorised(const NormArgs& a, bool f32) {
 cudaError_t norm_forward_launch(const NormArgs& a, int kind, bool f32, int sms,
                                 cudaStream_t stream) {
   if (norm_vectorised(a, f32))
-    return f32 ? by_width<float, true>(a, kind, sms, stream)
-               : by_width<__nv_bfloat16, true>(a, kind, sms, stream);
-  return f32 ? by_width<float, false>(a, kind, sms, stream)
-             : by_width<__nv_bfloat16, false>(a, kind, sms, stream);
+    return f32 ? launch<float, true>(a, kind, sms, stream)
+               : launch<__nv_bfloat16, true>(a, kind, sms, stream);
+  return f32 ? launch<float, false>(a, kind, sms, stream)
+             : launch<__nv_bfloat16, false>(a, kind, sms, stream);
 }
 
 }  // namespace infini
