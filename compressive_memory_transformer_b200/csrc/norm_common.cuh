@@ -125,7 +125,24 @@ __device__ __forceinline__ void store_row(void* base, long long row, int D, int 
 template <typename L>
 __device__ __forceinline__ Row16 load_param(const float* p, int D, int t) {
   Row16 r;
-  if constexpr (L::kPiece > 1) {
+  if constexpr (L::kPiece == 8) {
+    // 32 bytes per load: a warp reads whole lines (two 16-byte loads per thread read every
+    // line twice, and the L1 pipe was the busiest unit of the kernels). volatile keeps the
+    // load under its condition and its caller's: the compiler may execute other asm early,
+    // which for a load from an absent vector or past its end is an illegal access
+#pragma unroll
+    for (int e = 0; e < kE; e += 8) {
+      const int c = L::col(t, e);
+      float f[8] = {};
+      if (c < D)
+        asm volatile("ld.global.nc.v8.f32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+                     : "=f"(f[0]), "=f"(f[1]), "=f"(f[2]), "=f"(f[3]), "=f"(f[4]), "=f"(f[5]),
+                       "=f"(f[6]), "=f"(f[7])
+                     : "l"(p + c));
+#pragma unroll
+      for (int i = 0; i < 4; ++i) r.p[e / 2 + i] = f2pack(f[2 * i], f[2 * i + 1]);
+    }
+  } else if constexpr (L::kPiece > 1) {
 #pragma unroll
     for (int e = 0; e < kE; e += 4) {
       const int c = L::col(t, e);

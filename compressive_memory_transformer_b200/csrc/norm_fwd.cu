@@ -95,16 +95,20 @@ cudaError_t launch(const NormArgs& a, int kind, int sms, cudaStream_t stream) {
   });
 }
 
-bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+bool on(const void* p, uintptr_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
 
 }  // namespace
 
-// Every row of every array starts on 16 bytes.
+// Every row of every array starts on 16 bytes (and the vectors beside bf16 rows on 32).
 bool norm_vectorised(const NormArgs& a, bool f32) {
-  return a.D % (f32 ? 4 : 8) == 0 && aligned16(a.x) && aligned16(a.b) && aligned16(a.r) &&
-         aligned16(a.h) && aligned16(a.dr) && aligned16(a.dh) && aligned16(a.dx) &&
-         aligned16(a.db) && aligned16(a.gate) && aligned16(a.post_w) && aligned16(a.post_b) &&
-         aligned16(a.pre_w) && aligned16(a.pre_b);
+  bool ok = a.D % (f32 ? 4 : 8) == 0;
+  for (const void* p : {a.x, a.b, a.dr, a.dh, static_cast<const void*>(a.r),
+                        static_cast<const void*>(a.h), static_cast<const void*>(a.dx),
+                        static_cast<const void*>(a.db)})
+    ok = ok && on(p, 16);
+  for (const float* p : {a.gate, a.post_w, a.post_b, a.pre_w, a.pre_b})
+    ok = ok && on(p, f32 ? 16 : 32);
+  return ok;
 }
 
 cudaError_t norm_forward_launch(const NormArgs& a, int kind, bool f32, int sms,
