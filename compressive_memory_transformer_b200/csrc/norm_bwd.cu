@@ -22,20 +22,18 @@
 namespace infini {
 namespace {
 
-#ifndef NB_RES
-#define NB_RES 512
-#endif
-constexpr int kResident = NB_RES;  // threads per SM
+constexpr int kResident = 512;  // threads per SM: 128 registers each
+constexpr int kE = 16;          // elements per thread
 
-// Shared memory of a block's sums over rows.
-constexpr int acc_bytes(bool layer, int threads) {
-  return norm_sets(layer ? kNormLayer : kNormRms) * kP * threads * 8;
+// Shared memory of a block: its sums over rows, and gate times w (and c).
+constexpr int slots_bytes(bool layer, int threads) {
+  return (layer ? norm_sets(kNormLayer) + 2 : norm_sets(kNormRms) + 1) * (kE / 2) * threads * 8;
 }
 
 // The part of a norm's gradient that both norms share: with t the gradient of n(v) and vn =
 // n(v), t - [mean t] - vn mean(t vn), in place of t (to be multiplied by n's factor).
 template <bool LAYER, typename R>
-__device__ __forceinline__ void centre(Row16& t, const Row16& vn, float inv_d, R& red) {
+__device__ __forceinline__ void centre(Row<kE>& t, const Row<kE>& vn, float inv_d, R& red) {
   uint64_t s1 = 0, s2 = 0;
   INFINI_EACH_PAIR {
     s1 = fma2(t.p[i], vn.p[i], s1);
@@ -54,32 +52,52 @@ __device__ __forceinline__ void centre(Row16& t, const Row16& vn, float inv_d, R
 template <typename T, int TPR, bool VEC, bool LAYER>
 __global__ void __launch_bounds__(norm_threads(TPR), kResident / norm_threads(TPR))
 norm_backward_kernel(const NormArgs a) {
-  using L = RowLayout<T, TPR, VEC>;
+  using L = RowLayout<T, TPR, VEC, kE>;
   constexpr int kThreads = norm_threads(TPR), kWorkers = kThreads / TPR;
   constexpr int kSets = norm_sets(LAYER ? kNormLayer : kNormRms);
   __shared__ float2 sbuf[kWorkers][2][TPR / 32];
-  extern __shared__ uint64_t acc[];  // [set][pair][thread]
+  extern __shared__ uint64_t slots[];  // [set][pair][thread]
   const int w = threadIdx.x / TPR, t = threadIdx.x % TPR;
   RowSum<TPR> red{&sbuf[w], 1 + w};
   const int D = a.D;
   const float inv_d = 1.f / (float)D;
-  // sets: 0 dw_pre, 1 dw_post, 2 dc_pre, 3 dc_post
-  auto sum = [&](int set, int i) -> uint64_t& {
-    return acc[(set * kP + i) * kThreads + threadIdx.x];
+  // sets: 0 dw_pre, 1 dw_post, (2 dc_pre, 3 dc_post,) gate w (, gate c)
+  auto slot = [&](int set, int i) -> uint64_t& {
+    return slots[(set * (kE / 2) + i) * kThreads + threadIdx.x];
   };
 #pragma unroll
   for (int s = 0; s < kSets; ++s)
-    INFINI_EACH_PAIR sum(s, i) = 0;
+    INFINI_EACH_PAIR slot(s, i) = 0;
   const long long units = a.groups * a.cpg;
   for (long long u0 = (long long)blockIdx.x * kWorkers + w; u0 < units;
        u0 += (long long)gridDim.x * kWorkers) {
     const long long g = u0 / a.cpg, c = u0 % a.cpg;
     const long long r0 = g * a.group_rows + a.group_rows * c / a.cpg;
     const long long r1 = g * a.group_rows + a.group_rows * (c + 1) / a.cpg;
-    Row16 pn, pd;  // sums over the unit's rows of d bn and of d
+    // gate w and gate c of this unit's rows (w, the gate, or 1 alone where the others are
+    // absent): r = alpha x + (gate w) bn + gate c
+    const bool shift = LAYER && a.post_b != nullptr;
+    if (a.b) {
+      Row<kE> q, k;
+      INFINI_EACH_PAIR q.p[i] = both(1.f);
+      if (a.post_w) q = load_param<L>(a.post_w, D, t);
+      if (shift) k = load_param<L>(a.post_b, D, t);
+      if (a.gate) {
+        const Row<kE> f = load_param<L>(a.gate + g * D, D, t);
+        INFINI_EACH_PAIR {
+          q.p[i] = mul2(q.p[i], f.p[i]);
+          if (shift) k.p[i] = mul2(k.p[i], f.p[i]);
+        }
+      }
+      INFINI_EACH_PAIR {
+        slot(kSets, i) = q.p[i];
+        if (shift) slot(kSets + 1, i) = k.p[i];
+      }
+    }
+    Row<kE> pn, pd;  // sums over the unit's rows of d bn and of d
     INFINI_EACH_PAIR pn.p[i] = pd.p[i] = 0;
     for (long long row = r0; row < r1; ++row) {
-      RowRaw<T, TPR, VEC> rx, rb, rr, rh;
+      RowRaw<T, TPR, VEC, kE> rx, rb, rr, rh;
       rx.load(a.x, row, D, t);
       if (a.b) rb.load(a.b, row, D, t);
       // dh, and dr later, when registers are free again (fp32: both later)
@@ -90,47 +108,35 @@ norm_backward_kernel(const NormArgs a) {
         if (a.dh) prefetch_row<T>(a.dh, row + 1, D);
         if (a.dr) prefetch_row<T>(a.dr, row + 1, D);
       }
-      Row16 v = rx.get(), bn;
+      Row<kE> v = rx.get(), bn;
       float inv_b = 1.f;
       INFINI_EACH_PAIR v.p[i] = mul2(v.p[i], both(a.alpha));
       if (a.b) {
         bn = rb.get();
-        Row16 u = bn;
-        if (a.post_w) {
-          inv_b = normalise<L, LAYER>(bn, t, D, inv_d, a.eps, red);
-          const Row16 q = load_param<L>(a.post_w, D, t);
-          if (LAYER && a.post_b) {
-            const Row16 k = load_param<L>(a.post_b, D, t);
-            INFINI_EACH_PAIR u.p[i] = fma2(bn.p[i], q.p[i], k.p[i]);
-          } else {
-            INFINI_EACH_PAIR u.p[i] = mul2(bn.p[i], q.p[i]);
-          }
-        }
-        if (a.gate) {
-          const Row16 q = load_param<L>(a.gate + g * D, D, t);
-          INFINI_EACH_PAIR v.p[i] = fma2(q.p[i], u.p[i], v.p[i]);
-        } else {
-          INFINI_EACH_PAIR v.p[i] = add2(u.p[i], v.p[i]);
+        if (a.post_w) inv_b = normalise<L, LAYER>(bn, t, D, inv_d, a.eps, red);
+        INFINI_EACH_PAIR {
+          v.p[i] = fma2(slot(kSets, i), bn.p[i], v.p[i]);
+          if (shift) v.p[i] = add2(v.p[i], slot(kSets + 1, i));
         }
       }
       if (a.dr) rr.load(a.dr, row, D, t);
-      Row16 d;
+      Row<kE> d;
       INFINI_EACH_PAIR d.p[i] = 0;
       if (a.dh) {
         if (sizeof(T) == 4) rh.load(a.dh, row, D, t);
         const uint64_t inv_r = both(normalise<L, LAYER>(v, t, D, inv_d, a.eps, red));
-        Row16 h = rh.get();
-        const Row16 q = load_param<L>(a.pre_w, D, t);
+        Row<kE> h = rh.get();
+        const Row<kE> q = load_param<L>(a.pre_w, D, t);
         INFINI_EACH_PAIR {
-          sum(0, i) = fma2(h.p[i], v.p[i], sum(0, i));
-          if constexpr (LAYER) sum(2, i) = add2(sum(2, i), h.p[i]);
+          slot(0, i) = fma2(h.p[i], v.p[i], slot(0, i));
+          if constexpr (LAYER) slot(2, i) = add2(slot(2, i), h.p[i]);
           h.p[i] = mul2(h.p[i], q.p[i]);
         }
         centre<LAYER>(h, v, inv_d, red);
         INFINI_EACH_PAIR d.p[i] = mul2(h.p[i], inv_r);
       }
       if (a.dr) {
-        const Row16 k = rr.get();
+        const Row<kE> k = rr.get();
         INFINI_EACH_PAIR d.p[i] = add2(d.p[i], k.p[i]);
       }
       if (a.dx) {
@@ -141,14 +147,9 @@ norm_backward_kernel(const NormArgs a) {
       INFINI_EACH_PAIR {
         pn.p[i] = fma2(d.p[i], bn.p[i], pn.p[i]);
         if constexpr (LAYER) pd.p[i] = add2(pd.p[i], d.p[i]);
-      }
-      if (a.gate) {
-        const Row16 q = load_param<L>(a.gate + g * D, D, t);
-        INFINI_EACH_PAIR d.p[i] = mul2(d.p[i], q.p[i]);
+        d.p[i] = mul2(d.p[i], slot(kSets, i));
       }
       if (a.post_w) {
-        const Row16 q = load_param<L>(a.post_w, D, t);
-        INFINI_EACH_PAIR d.p[i] = mul2(d.p[i], q.p[i]);
         centre<LAYER>(d, bn, inv_d, red);
         INFINI_EACH_PAIR d.p[i] = mul2(d.p[i], both(inv_b));
       }
@@ -156,25 +157,25 @@ norm_backward_kernel(const NormArgs a) {
     }
     // the unit's rows share a gate row
     if (a.post_w) {
-      Row16 e = pn, f = pd;
+      Row<kE> e = pn, f = pd;
       if (a.gate) {
-        const Row16 q = load_param<L>(a.gate + g * D, D, t);
+        const Row<kE> q = load_param<L>(a.gate + g * D, D, t);
         INFINI_EACH_PAIR {
           e.p[i] = mul2(e.p[i], q.p[i]);
           if constexpr (LAYER) f.p[i] = mul2(f.p[i], q.p[i]);
         }
       }
       INFINI_EACH_PAIR {
-        sum(1, i) = add2(sum(1, i), e.p[i]);
-        if constexpr (LAYER) sum(3, i) = add2(sum(3, i), f.p[i]);
+        slot(1, i) = add2(slot(1, i), e.p[i]);
+        if constexpr (LAYER) slot(3, i) = add2(slot(3, i), f.p[i]);
       }
     }
     if (a.gpart) {
       if (a.post_w) {
-        const Row16 q = load_param<L>(a.post_w, D, t);
+        const Row<kE> q = load_param<L>(a.post_w, D, t);
         INFINI_EACH_PAIR pn.p[i] = mul2(pn.p[i], q.p[i]);
         if (LAYER && a.post_b) {
-          const Row16 k = load_param<L>(a.post_b, D, t);
+          const Row<kE> k = load_param<L>(a.post_b, D, t);
           INFINI_EACH_PAIR pn.p[i] = fma2(pd.p[i], k.p[i], pn.p[i]);
         }
       }
@@ -192,13 +193,25 @@ norm_backward_kernel(const NormArgs a) {
   for (int s = 0; s < kSets; ++s) {
     float* dst = a.part + ((long long)blockIdx.x * kSets + s) * D;
     INFINI_EACH_PAIR {
-      uint64_t v = sum(s, i);
+      uint64_t v = slot(s, i);
 #pragma unroll
       for (int k = 1; k < kWorkers; ++k)
-        v = add2(v, acc[(s * kP + i) * kThreads + k * TPR + t]);
+        v = add2(v, slots[(s * (kE / 2) + i) * kThreads + k * TPR + t]);
       if (L::col(t, 2 * i) < D) dst[L::col(t, 2 * i)] = lo_of(v);
       if (L::col(t, 2 * i + 1) < D) dst[L::col(t, 2 * i + 1)] = hi_of(v);
     }
+  }
+}
+
+// f(threads per row) for a width.
+template <typename F>
+cudaError_t with_tpr(int D, F&& f) {
+  switch (norm_tpr(D, kE)) {
+    case 32: return f(std::integral_constant<int, 32>{});
+    case 64: return f(std::integral_constant<int, 64>{});
+    case 128: return f(std::integral_constant<int, 128>{});
+    case 256: return f(std::integral_constant<int, 256>{});
+    default: return f(std::integral_constant<int, 512>{});
   }
 }
 
@@ -207,7 +220,7 @@ cudaError_t launch(const NormArgs& a, int blocks, cudaStream_t stream) {
   return with_tpr(a.D, [&](auto tpr) {
     constexpr int TPR = decltype(tpr)::value, kThreads = norm_threads(TPR);
     norm_backward_kernel<T, TPR, VEC, LAYER>
-        <<<blocks, kThreads, acc_bytes(LAYER, kThreads), stream>>>(a);
+        <<<blocks, kThreads, slots_bytes(LAYER, kThreads), stream>>>(a);
     return cudaGetLastError();
   });
 }
@@ -220,7 +233,7 @@ cudaError_t allow() {
       constexpr int TPR = decltype(tpr)::value;
       return cudaFuncSetAttribute(norm_backward_kernel<T, TPR, VEC, LAYER>,
                                   cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                  acc_bytes(LAYER, norm_threads(TPR)));
+                                  slots_bytes(LAYER, norm_threads(TPR)));
     });
     if (e == cudaSuccess) e = f;
   }
@@ -250,7 +263,7 @@ gate_sum_kernel(const float* __restrict__ gpart, float* __restrict__ dgate, long
 
 void norm_backward_plan(long long rows, int D, long long groups, int sms, int* blocks,
                         long long* cpg) {
-  const int threads = norm_threads(norm_tpr(D)), workers = threads / norm_tpr(D);
+  const int threads = norm_threads(norm_tpr(D, kE)), workers = threads / norm_tpr(D, kE);
   const long long per_sm = kResident / threads;
   long long nb = (rows + workers - 1) / workers;
   if (nb > per_sm * sms) nb = per_sm * sms;

@@ -1,12 +1,12 @@
 // norm_common.cuh — what the norm kernels share: the layout of a row over its threads,
 // loads and stores, and sums over a row's threads.
 //
-// A row of D elements belongs to TPR threads of a block (a "worker"); each thread holds 16
-// elements as 8 fp32 pairs, on which the arithmetic is packed (f32x2). Vector layout
+// A row of D elements belongs to TPR threads of a block (a "worker"); each thread holds E
+// (16 or 32) elements as fp32 pairs, on which the arithmetic is packed (f32x2). Vector layout
 // (16-byte pieces): piece j of thread t is the (t + j TPR)-th of the row, so that
 // neighbouring threads read neighbouring pieces; 8 elements each of bf16, 4 of fp32. Scalar
 // layout, for odd widths and rows that do not start on 16 bytes: element t + i TPR for
-// i = 0..15. Elements outside the row are held as 0.
+// i = 0..E - 1. Elements outside the row are held as 0.
 #pragma once
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
@@ -18,9 +18,6 @@
 
 namespace infini {
 
-constexpr int kE = 16;      // elements of a row per thread
-constexpr int kP = kE / 2;  // pairs
-
 __device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
   uint64_t d;
   asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
@@ -30,13 +27,16 @@ __device__ __forceinline__ uint64_t both(float v) { return f2pack(v, v); }
 __device__ __forceinline__ float lo_of(uint64_t v) { return __uint_as_float((uint32_t)v); }
 __device__ __forceinline__ float hi_of(uint64_t v) { return __uint_as_float((uint32_t)(v >> 32)); }
 
-struct Row16 {
-  uint64_t p[kP];
+// A thread's elements of one row.
+template <int E>
+struct Row {
+  uint64_t p[E / 2];
 };
-#define INFINI_EACH_PAIR _Pragma("unroll") for (int i = 0; i < kP; ++i)
+#define INFINI_EACH_PAIR _Pragma("unroll") for (int i = 0; i < kE / 2; ++i)
 
-template <typename T, int TPR, bool VEC>
+template <typename T, int TPR, bool VEC, int E>
 struct RowLayout {
+  static constexpr int kE = E;
   static constexpr int kPiece = VEC ? 16 / (int)sizeof(T) : 1;  // elements of a piece
   static constexpr int kPieces = kE / kPiece;
   // Column of element e of thread t.
@@ -45,10 +45,10 @@ struct RowLayout {
   }
 };
 
-// One row's elements of one thread as loaded (32 bytes of bf16, 64 of fp32).
-template <typename T, int TPR, bool VEC>
+// One row's elements of one thread as loaded.
+template <typename T, int TPR, bool VEC, int kE>
 struct RowRaw {
-  using L = RowLayout<T, TPR, VEC>;
+  using L = RowLayout<T, TPR, VEC, kE>;
   uint32_t w[kE * sizeof(T) / 4];
 
   __device__ __forceinline__ void load(const void* base, long long row, int D, int t) {
@@ -75,8 +75,8 @@ struct RowRaw {
       }
     }
   }
-  __device__ __forceinline__ Row16 get() const {
-    Row16 r;
+  __device__ __forceinline__ Row<kE> get() const {
+    Row<kE> r;
     INFINI_EACH_PAIR {
       if constexpr (sizeof(T) == 4)
         r.p[i] = (uint64_t)w[2 * i] | ((uint64_t)w[2 * i + 1] << 32);
@@ -87,10 +87,10 @@ struct RowRaw {
   }
 };
 
-template <typename T, int TPR, bool VEC>
+template <typename T, int TPR, bool VEC, int kE>
 __device__ __forceinline__ void store_row(void* base, long long row, int D, int t,
-                                          const Row16& v) {
-  using L = RowLayout<T, TPR, VEC>;
+                                          const Row<kE>& v) {
+  using L = RowLayout<T, TPR, VEC, kE>;
   T* p = static_cast<T*>(base) + row * D;
   if constexpr (VEC) {
 #pragma unroll
@@ -123,8 +123,9 @@ __device__ __forceinline__ void store_row(void* base, long long row, int D, int 
 
 // A vector of fp32 parameters in the row's layout.
 template <typename L>
-__device__ __forceinline__ Row16 load_param(const float* p, int D, int t) {
-  Row16 r;
+__device__ __forceinline__ Row<L::kE> load_param(const float* p, int D, int t) {
+  constexpr int kE = L::kE;
+  Row<kE> r;
   if constexpr (L::kPiece == 8) {
     // 32 bytes per load: a warp reads whole lines (two 16-byte loads per thread read every
     // line twice, and the L1 pipe was the busiest unit of the kernels). volatile keeps the
@@ -212,12 +213,13 @@ __device__ __forceinline__ float halves(uint64_t v) { return lo_of(v) + hi_of(v)
 // v -> (v - mean) / sd or v / rms; elements outside the row stay 0. The variance is the
 // mean of the squared distances from the mean (a second sum), never E v^2 - mean^2.
 template <typename L, bool LAYER, typename R>
-__device__ __forceinline__ float normalise(Row16& v, int t, int D, float inv_d, float eps,
+__device__ __forceinline__ float normalise(Row<L::kE>& v, int t, int D, float inv_d, float eps,
                                            R& red) {
+  constexpr int kE = L::kE;
   if constexpr (LAYER) {
     uint64_t s = v.p[0];
 #pragma unroll
-    for (int i = 1; i < kP; ++i) s = add2(s, v.p[i]);
+    for (int i = 1; i < kE / 2; ++i) s = add2(s, v.p[i]);
     const float mean = red.sum(halves(s)) * inv_d;
     INFINI_EACH_PAIR {
       const uint64_t c = add2(v.p[i], both(-mean));
@@ -241,22 +243,12 @@ __device__ __forceinline__ void prefetch_row(const void* base, long long row, in
                : "memory");
 }
 
-// Threads per row for a width, and threads per block.
-constexpr int norm_tpr(int D) {
-  return D <= 512 ? 32 : D <= 1024 ? 64 : D <= 2048 ? 128 : D <= 4096 ? 256 : 512;
+// Threads per row for a width and a number of elements per thread, and threads per block.
+constexpr int norm_tpr(int D, int E) {
+  int t = 32;
+  while (t * E < D) t *= 2;
+  return t;
 }
 constexpr int norm_threads(int tpr) { return tpr < 256 ? 256 : tpr; }
-
-// f(threads per row) for a width.
-template <typename F>
-cudaError_t with_tpr(int D, F&& f) {
-  switch (norm_tpr(D)) {
-    case 32: return f(std::integral_constant<int, 32>{});
-    case 64: return f(std::integral_constant<int, 64>{});
-    case 128: return f(std::integral_constant<int, 128>{});
-    case 256: return f(std::integral_constant<int, 256>{});
-    default: return f(std::integral_constant<int, 512>{});
-  }
-}
 
 }  // namespace infini

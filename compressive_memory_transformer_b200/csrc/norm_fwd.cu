@@ -14,16 +14,19 @@
 namespace infini {
 namespace {
 
-#ifndef NF_RES
-#define NF_RES 512
-#endif
-constexpr int kResident = NF_RES;  // threads per SM
+constexpr int kResident = 512;  // threads per SM: 128 registers each
 
-template <typename T, int TPR, bool VEC, bool LAYER>
+template <typename T, int TPR, bool VEC, int kE, bool LAYER>
 __global__ void __launch_bounds__(norm_threads(TPR), kResident / norm_threads(TPR))
 norm_forward_kernel(const NormArgs a) {
-  using L = RowLayout<T, TPR, VEC>;
+  using L = RowLayout<T, TPR, VEC, kE>;
   constexpr int kWorkers = norm_threads(TPR) / TPR;
+  // the row after next in L2 early: 8 rows of 1024 bf16 in flight are too few for an SM's
+  // share of the bandwidth (205 -> 172 us for 131072 of them); fp32 rows have twice the
+  // bytes and lose by it (170 -> 186 us for 65536)
+  constexpr bool kAhead = VEC && sizeof(T) == 2;
+  // the next row in registers (32 elements per thread leave no room: from L2 then)
+  constexpr bool kHold = kE == 16;
   __shared__ float2 sbuf[kWorkers][2][TPR / 32];
   const int w = threadIdx.x / TPR, t = threadIdx.x % TPR;
   RowSum<TPR> red{&sbuf[w], 1 + w};
@@ -31,45 +34,54 @@ norm_forward_kernel(const NormArgs a) {
   const int D = a.D;
   const long long step = (long long)gridDim.x * kWorkers;
   long long row = (long long)blockIdx.x * kWorkers + w;
-  RowRaw<T, TPR, VEC> nx, nb;
-  if (row < a.rows) {
+  RowRaw<T, TPR, VEC, kE> nx, nb;
+  if (kHold && row < a.rows) {
     nx.load(a.x, row, D, t);
     if (a.b) nb.load(a.b, row, D, t);
   }
   for (; row < a.rows; row += step) {
-    Row16 v = nx.get();
+    if (!kHold) {
+      nx.load(a.x, row, D, t);
+      if (a.b) nb.load(a.b, row, D, t);
+    }
+    const long long ahead = row + (kHold ? 2 : 1) * step;
+    if (kAhead && t == 0 && ahead < a.rows) {
+      prefetch_row<T>(a.x, ahead, D);
+      if (a.b) prefetch_row<T>(a.b, ahead, D);
+    }
+    Row<kE> v = nx.get();
     INFINI_EACH_PAIR v.p[i] = mul2(v.p[i], both(a.alpha));
     if (a.b) {
-      Row16 u = nb.get();
-      if (row + step < a.rows) {
+      Row<kE> u = nb.get();
+      if (kHold && row + step < a.rows) {
         nx.load(a.x, row + step, D, t);
         nb.load(a.b, row + step, D, t);
       }
       if (a.post_w) {
         normalise<L, LAYER>(u, t, D, inv_d, a.eps, red);
-        const Row16 q = load_param<L>(a.post_w, D, t);
+        const Row<kE> q = load_param<L>(a.post_w, D, t);
         if (a.post_b) {
-          const Row16 c = load_param<L>(a.post_b, D, t);
+          const Row<kE> c = load_param<L>(a.post_b, D, t);
           INFINI_EACH_PAIR u.p[i] = fma2(u.p[i], q.p[i], c.p[i]);
         } else {
           INFINI_EACH_PAIR u.p[i] = mul2(u.p[i], q.p[i]);
         }
       }
       if (a.gate) {
-        const Row16 q = load_param<L>(a.gate + (row / a.group_rows) * D, D, t);
+        const Row<kE> q = load_param<L>(a.gate + (row / a.group_rows) * D, D, t);
         INFINI_EACH_PAIR v.p[i] = fma2(u.p[i], q.p[i], v.p[i]);
       } else {
         INFINI_EACH_PAIR v.p[i] = add2(u.p[i], v.p[i]);
       }
-    } else if (row + step < a.rows) {
+    } else if (kHold && row + step < a.rows) {
       nx.load(a.x, row + step, D, t);
     }
     if (a.r) store_row<T, TPR, VEC>(a.r, row, D, t, v);
     if (a.h) {
       normalise<L, LAYER>(v, t, D, inv_d, a.eps, red);
-      const Row16 q = load_param<L>(a.pre_w, D, t);
+      const Row<kE> q = load_param<L>(a.pre_w, D, t);
       if (a.pre_b) {
-        const Row16 c = load_param<L>(a.pre_b, D, t);
+        const Row<kE> c = load_param<L>(a.pre_b, D, t);
         INFINI_EACH_PAIR v.p[i] = fma2(v.p[i], q.p[i], c.p[i]);
       } else {
         INFINI_EACH_PAIR v.p[i] = mul2(v.p[i], q.p[i]);
@@ -79,20 +91,40 @@ norm_forward_kernel(const NormArgs a) {
   }
 }
 
-template <typename T, bool VEC>
+template <typename T, int TPR, bool VEC, int E>
 cudaError_t launch(const NormArgs& a, int kind, int sms, cudaStream_t stream) {
-  return with_tpr(a.D, [&](auto tpr) {
-    constexpr int TPR = decltype(tpr)::value;
-    constexpr int kThreads = norm_threads(TPR), kWorkers = kThreads / TPR;
-    const long long need = (a.rows + kWorkers - 1) / kWorkers;
-    const long long most = (long long)sms * (kResident / kThreads);
-    const unsigned grid = (unsigned)(need < most ? need : most);
-    if (kind == kNormLayer)
-      norm_forward_kernel<T, TPR, VEC, true><<<grid, kThreads, 0, stream>>>(a);
-    else
-      norm_forward_kernel<T, TPR, VEC, false><<<grid, kThreads, 0, stream>>>(a);
-    return cudaGetLastError();
-  });
+  constexpr int kThreads = norm_threads(TPR), kWorkers = kThreads / TPR;
+  const long long need = (a.rows + kWorkers - 1) / kWorkers;
+  const long long most = (long long)sms * (kResident / kThreads);
+  const unsigned grid = (unsigned)(need < most ? need : most);
+  if (kind == kNormLayer)
+    norm_forward_kernel<T, TPR, VEC, E, true><<<grid, kThreads, 0, stream>>>(a);
+  else
+    norm_forward_kernel<T, TPR, VEC, E, false><<<grid, kThreads, 0, stream>>>(a);
+  return cudaGetLastError();
+}
+
+// Elements per thread: 16; for wide bf16 rows 32, which keeps twice the rows in work at a
+// time and halves the warps of a row's sums (32768 x 4096: 213 -> 196 us, 16384 x 8192: 255
+// -> 210; 65536 x 2048 would lose, 173 -> 187).
+template <typename T, bool VEC>
+cudaError_t by_width(const NormArgs& a, int kind, int sms, cudaStream_t stream) {
+  if constexpr (VEC && sizeof(T) == 2) {
+    if (a.D > 2048) {
+      switch (norm_tpr(a.D, 32)) {
+        case 64: return launch<T, 64, VEC, 32>(a, kind, sms, stream);
+        case 128: return launch<T, 128, VEC, 32>(a, kind, sms, stream);
+        default: return launch<T, 256, VEC, 32>(a, kind, sms, stream);
+      }
+    }
+  }
+  switch (norm_tpr(a.D, 16)) {
+    case 32: return launch<T, 32, VEC, 16>(a, kind, sms, stream);
+    case 64: return launch<T, 64, VEC, 16>(a, kind, sms, stream);
+    case 128: return launch<T, 128, VEC, 16>(a, kind, sms, stream);
+    case 256: return launch<T, 256, VEC, 16>(a, kind, sms, stream);
+    default: return launch<T, 512, VEC, 16>(a, kind, sms, stream);
+  }
 }
 
 bool on(const void* p, uintptr_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
@@ -114,10 +146,10 @@ bool norm_vectorised(const NormArgs& a, bool f32) {
 cudaError_t norm_forward_launch(const NormArgs& a, int kind, bool f32, int sms,
                                 cudaStream_t stream) {
   if (norm_vectorised(a, f32))
-    return f32 ? launch<float, true>(a, kind, sms, stream)
-               : launch<__nv_bfloat16, true>(a, kind, sms, stream);
-  return f32 ? launch<float, false>(a, kind, sms, stream)
-             : launch<__nv_bfloat16, false>(a, kind, sms, stream);
+    return f32 ? by_width<float, true>(a, kind, sms, stream)
+               : by_width<__nv_bfloat16, true>(a, kind, sms, stream);
+  return f32 ? by_width<float, false>(a, kind, sms, stream)
+             : by_width<__nv_bfloat16, false>(a, kind, sms, stream);
 }
 
 }  // namespace infini
