@@ -73,13 +73,29 @@ struct Epilogue {
   int act;
 };
 
-__device__ __forceinline__ float4 ld_cluster_f4(uint32_t addr) {
-  float4 v;
-  asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
-               : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
-               : "r"(addr)
+// Stores into the shared memory of a block of this cluster (address in its window).
+__device__ __forceinline__ void st_cluster_f4(uint32_t addr, const uint32_t* v) {
+  asm volatile("st.shared::cluster.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(v[0]),
+               "r"(v[1]), "r"(v[2]), "r"(v[3])
                : "memory");
-  return v;
+}
+__device__ __forceinline__ void st_cluster_f1(uint32_t addr, uint32_t v) {
+  asm volatile("st.shared::cluster.b32 [%0], %1;" ::"r"(addr), "r"(v) : "memory");
+}
+
+// The address in the cluster's window of this block's shared address, in block `rank`.
+__device__ __forceinline__ uint32_t mapa(uint32_t addr, uint32_t rank) {
+  uint32_t r;
+  asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(addr), "r"(rank));
+  return r;
+}
+
+// The two halves of a barrier over all threads of the cluster.
+__device__ __forceinline__ void cluster_arrive() {
+  asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void cluster_wait() {
+  asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
 
 __device__ __forceinline__ float bf16_lo(uint32_t v) { return __uint_as_float(v << 16); }
@@ -122,58 +138,83 @@ __device__ __forceinline__ void finish8(float (&v)[8], const Epilogue& e, long l
 struct TileParams {
   unsigned tiles_b;  // BN-wide tiles along the B side
   int ksteps;        // of the whole reduction
-  int split;         // blocks (cluster size) sharing the reduction
+  int split;         // blocks (cluster size: 1, 2, 4 or 8) sharing the reduction
   long long rows, cols;  // of the output
   Epilogue epi;
 };
 
 constexpr int kTileThreads = 256;
-constexpr int tile_stages(int bn) { return bn <= 16 ? 10 : bn <= 32 ? 9 : bn <= 64 ? 8 : 6; }
+constexpr int tile_stages(int bn) { return bn <= 16 ? 10 : bn <= 32 ? 9 : bn <= 64 ? 7 : 5; }
 constexpr int tile_stage_bytes(int bn) { return (128 + bn) * 128; }
-constexpr int tile_smem(int bn) { return tile_stages(bn) * tile_stage_bytes(bn) + 256 + 1024; }
-// the fp32 tile that the ring's memory holds after the products: rows of (columns + 4)
-static_assert(128 * (128 + 4) * 4 <= tile_stages(128) * tile_stage_bytes(128), "tile fits");
-static_assert(128 * (64 + 4) * 4 <= tile_stages(64) * tile_stage_bytes(64), "tile fits");
-static_assert(32 * (128 + 4) * 4 <= tile_stages(32) * tile_stage_bytes(32), "tile fits");
-static_assert(16 * (128 + 4) * 4 <= tile_stages(16) * tile_stage_bytes(16), "tile fits");
+constexpr int tile_ring(int bn) { return tile_stages(bn) * tile_stage_bytes(bn); }
+// ring, partial sums of the block's share of the tile, barriers, alignment
+constexpr int tile_smem(int bn) { return tile_ring(bn) + 128 * bn * 4 + 256 + 1024; }
+static_assert(tile_smem(128) <= 232448 && tile_smem(64) <= 232448, "shared memory of a block");
 
-// Warps 0-3 drain the accumulator, warp 4 brings the operands (TMA), warp 5 issues the
-// products; all eight warps share the epilogue, which goes through shared memory: the
-// accumulator's lanes are output rows (or, with SWAP, output columns), and the pass
-// through an fp32 tile gives whole 16-byte pieces of output rows to neighbouring threads
-// in both cases, and a place from which the blocks of a cluster add their partial sums.
-// Bound by the stream of the weights with few rows: every block keeps its whole ring
-// (160 to 192 KB) in flight.
+// Warp 4 brings the operands (TMA), warp 5 issues the products; then all eight warps share
+// the epilogue (warp w drains accumulator lanes 32 (w % 4)..; warps 4-7 the upper half of
+// its columns). The blocks of a cluster split the reduction; each owns an equal share of
+// the tile's columns (rows with SWAP) and gets the others' partial sums of it stored into
+// its shared memory, so that one cluster barrier is all that the exchange takes, and adds
+// them in rank order, the same sums every time. A block alone with !SWAP, whose accumulator
+// lanes are output rows, writes straight from registers; with SWAP the same exchange turns
+// the tile round.
+// Bound by latency when small (the operands' first bytes, one pass through the tensor
+// cores, the exchange) and by the stream of the weights with few rows: every block keeps
+// its whole ring (160 to 180 KB) in flight.
 template <int BN, bool SWAP, bool A_MN, bool B_MN>
 __global__ void __launch_bounds__(kTileThreads, 1)
 linear_tile_kernel(const __grid_constant__ CUtensorMap tm_a,
                    const __grid_constant__ CUtensorMap tm_b, const TileParams p) {
   constexpr int ST = tile_stages(BN);
   constexpr int kABytes = 128 * 128, kStage = tile_stage_bytes(BN);
-  constexpr int kTileRows = SWAP ? BN : 128, kTileCols = SWAP ? 128 : BN;
-  constexpr int kLd = kTileCols + 4;  // floats; 4 of padding keep 16-byte row writes apart
   constexpr uint32_t kTmemCols = BN < 32 ? 32 : BN;
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                              ~uintptr_t(1023));
-  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + ST * kStage);
+  uint8_t* recv = smem + tile_ring(BN);
+  uint64_t* bars = reinterpret_cast<uint64_t*>(recv + 128 * BN * 4);
   uint64_t *full = bars, *empty = bars + ST, *acc = bars + 2 * ST;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(acc + 1);
-  float* tile = reinterpret_cast<float*>(smem);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const unsigned rank = p.split > 1 ? cluster_ctarank() : 0u;
+  const unsigned rank = cluster_ctarank();
   const unsigned t = blockIdx.x / (unsigned)p.split;
   const int a0 = 128 * (int)(t / p.tiles_b), b0 = BN * (int)(t % p.tiles_b);
   const int ks0 = (int)((long long)p.ksteps * rank / p.split);
   const int ks1 = (int)((long long)p.ksteps * (rank + 1) / p.split);
+  int issued = 0;
 
-  if (threadIdx.x == 0) {
-    for (int x = 0; x < 2 * ST + 1; ++x) mbar_init(&bars[x], 1);
-    fence_barrier_init();
-    tma_prefetch_desc(&tm_a);
-    tma_prefetch_desc(&tm_b);
-  }
-  if (warp == 5) {
+  auto load = [&](int st) {
+    uint8_t* sa = smem + st * kStage;
+    uint8_t* sb = sa + kABytes;
+    const int k = kKStep * (ks0 + issued);
+    mbar_arrive_expect_tx(&full[st], (uint32_t)kStage);
+    if (A_MN) {
+      tma_load_tile(sa, &tm_a, &full[st], a0, k);
+      tma_load_tile(sa + 8192, &tm_a, &full[st], a0 + 64, k);
+    } else {
+      tma_load_tile(sa, &tm_a, &full[st], k, a0);
+    }
+    if (B_MN) {
+#pragma unroll
+      for (int i = 0; i < (BN + 63) / 64; ++i)
+        tma_load_tile(sb + 8192 * i, &tm_b, &full[st], b0 + 64 * i, k);
+    } else {
+      tma_load_tile(sb, &tm_b, &full[st], k, b0);
+    }
+    ++issued;
+  };
+
+  cluster_arrive();  // waited for before the exchange: every block has started by then
+  if (warp == 4) {
+    if (lane == 0) {
+      // the first copies are on their way before the block has set up the rest
+      for (int x = 0; x < 2 * ST + 1; ++x) mbar_init(&bars[x], 1);
+      fence_barrier_init();
+      while (issued < ST && ks0 + issued < ks1) load(issued);
+    }
+    __syncwarp();
+  } else if (warp == 5) {
     tmem_alloc(tmem_slot, kTmemCols);
     tmem_relinquish();
   }
@@ -184,29 +225,12 @@ linear_tile_kernel(const __grid_constant__ CUtensorMap tm_a,
 
   if (warp == 4) {
     if (lane == 0) {
-      int issued = 0;
-      for (int ks = ks0; ks < ks1; ++ks, ++issued) {
-        const int st = issued % ST, use = issued / ST;
-        if (use > 0 && !mbar_wait(&empty[st], (uint32_t)((use - 1) & 1))) break;
-        uint8_t* sa = smem + st * kStage;
-        uint8_t* sb = sa + kABytes;
-        const int k = kKStep * ks;
-        mbar_arrive_expect_tx(&full[st], (uint32_t)kStage);
-        if (A_MN) {
-          tma_load_tile(sa, &tm_a, &full[st], a0, k);
-          tma_load_tile(sa + 8192, &tm_a, &full[st], a0 + 64, k);
-        } else {
-          tma_load_tile(sa, &tm_a, &full[st], k, a0);
-        }
-        if (B_MN) {
-#pragma unroll
-          for (int i = 0; i < (BN + 63) / 64; ++i)
-            tma_load_tile(sb + 8192 * i, &tm_b, &full[st], b0 + 64 * i, k);
-        } else {
-          tma_load_tile(sb, &tm_b, &full[st], k, b0);
-        }
+      while (ks0 + issued < ks1) {
+        const int st = issued % ST;
+        if (!mbar_wait(&empty[st], (uint32_t)((issued / ST - 1) & 1))) break;
+        load(st);
       }
-      // every copy into this block's ring has landed before the ring is reused or left
+      // every copy into this block's ring has landed before the block leaves
       for (int st = 0; st < ST && st < issued; ++st)
         drain_wait(&full[st], (uint32_t)(((issued - 1 - st) / ST) & 1));
     }
@@ -228,74 +252,120 @@ linear_tile_kernel(const __grid_constant__ CUtensorMap tm_a,
       __syncwarp();
       if (++st == ST) st = 0, phase ^= 1;
     }
-    if (elect_one()) mma_commit(acc);  // all products done: sums complete, ring free
+    if (elect_one()) mma_commit(acc);
     __syncwarp();
   }
-  // the products are done (for every warp: the ring's memory becomes the fp32 tile)
-  mbar_wait_warp(acc, 0);
-  __syncthreads();
-  if (warp < 4) {
-    tc_fence_after();
-    const int m = warp * 32 + lane;  // index along the 128 side
+  mbar_wait_warp(acc, 0);  // the sums are complete
+  tc_fence_after();
+
+  const int m = 32 * (warp & 3) + lane;  // index along the 128 side
+  const uint32_t lanes = (uint32_t)(32 * (warp & 3)) << 16;
+  constexpr int kCols = BN >= 64 ? BN / 2 : BN;  // accumulator columns of a warp
+  const int c0 = BN >= 64 ? kCols * (warp >> 2) : 0;
+  const bool drains = BN >= 64 || warp < 4;
+  if (!SWAP && p.split == 1) {
+    cluster_wait();
 #pragma unroll
-    for (int c = 0; c < BN; c += 32) {
-      uint32_t v[32];
-      tmem_ld32(tmem + ((uint32_t)(warp * 32) << 16) + (uint32_t)c, v);
+    for (int c = 0; c < kCols; c += 32) {
+      uint32_t a[32];
+      tmem_ld32(tmem + lanes + (uint32_t)(c0 + c), a);
       tmem_wait_ld();
-      if (SWAP) {
+      if ((long long)a0 + m < p.rows) {
 #pragma unroll
-        for (int i = 0; i < 32; ++i)
-          if (c + i < BN) tile[(c + i) * kLd + m] = __uint_as_float(v[i]);
-      } else {
+        for (int i = 0; i < 32; i += 8) {
+          if ((long long)b0 + c0 + c + i >= p.cols) continue;
+          float v[8];
 #pragma unroll
-        for (int i = 0; i < 32; i += 4)
-          *reinterpret_cast<uint4*>(&tile[m * kLd + c + i]) =
-              make_uint4(v[i], v[i + 1], v[i + 2], v[i + 3]);
+          for (int j = 0; j < 8; ++j) v[j] = __uint_as_float(a[i + j]);
+          finish8(v, p.epi, (long long)a0 + m, (long long)b0 + c0 + c + i);
+        }
       }
     }
     tc_fence_before();
+  } else {
+    cluster_wait();
+    const uint32_t log_s = 31u - (uint32_t)__clz(p.split);
+    const uint32_t dst = smem_u32(recv);
+    if (drains) {
+#pragma unroll
+      for (int c = 0; c < kCols; c += 32) {
+        uint32_t a[32];
+        tmem_ld32(tmem + lanes + (uint32_t)(c0 + c), a);
+        tmem_wait_ld();
+        if (SWAP) {
+          // share of rank q: rows [q BN / S, ..) of BN; from rank r: [r][row][128]
+          const uint32_t per = BN >> log_s;
+#pragma unroll
+          for (int i = 0; i < 32; ++i) {
+            const uint32_t r = (uint32_t)(c0 + c + i);
+            if (r < BN && (long long)b0 + r < p.rows)
+              st_cluster_f1(mapa(dst + ((rank * per + r % per) * 128 + (uint32_t)m) * 4, r / per),
+                            a[i]);
+          }
+        } else {
+          // share of rank q: columns [q BN / S, ..); from rank r: [r][128 rows][BN / S],
+          // 16-byte units of a row swizzled
+          const uint32_t per = (uint32_t)BN >> log_s, units = per / 4;
+          const uint32_t x = (units >= 8 ? (uint32_t)m : (uint32_t)m >> 1) & (units >= 8 ? 7u : 3u);
+          if ((long long)a0 + m < p.rows) {
+#pragma unroll
+            for (int i = 0; i < 32; i += 4) {
+              const uint32_t col = (uint32_t)(c0 + c + i), u = (col % per) / 4;
+              st_cluster_f4(mapa(dst + ((rank * 128 + (uint32_t)m) * units + (u ^ x)) * 16, col / per),
+                            a + i);
+            }
+          }
+        }
+      }
+    }
+    tc_fence_before();
+    __syncwarp();
+    cluster_arrive();
+    cluster_wait();
+    auto finish = [&](auto split) {
+      constexpr uint32_t S = decltype(split)::value;
+      constexpr uint32_t per = BN / S;
+      const float4* src = reinterpret_cast<const float4*>(recv);
+      constexpr uint32_t total = 128 * per / 8;  // pieces of 8 columns
+#pragma unroll 2
+      for (uint32_t u = threadIdx.x; u < total; u += kTileThreads) {
+        const uint32_t row = SWAP ? u / 16 : u / (per / 8), c8 = SWAP ? u % 16 : u % (per / 8);
+        const long long orow = SWAP ? (long long)b0 + rank * per + row : (long long)a0 + row;
+        const long long ocol = SWAP ? (long long)a0 + 8 * c8 : (long long)b0 + rank * per + 8 * c8;
+        if (orow >= p.rows || ocol >= p.cols) continue;
+        float4 x[S], y[S];
+#pragma unroll
+        for (uint32_t q = 0; q < S; ++q) {
+          if (SWAP) {
+            x[q] = src[(q * per + row) * 32 + 2 * c8];
+            y[q] = src[(q * per + row) * 32 + 2 * c8 + 1];
+          } else {
+            constexpr uint32_t units = per / 4;
+            const uint32_t z = (units >= 8 ? row : row >> 1) & (units >= 8 ? 7u : 3u);
+            x[q] = src[(q * 128 + row) * units + ((2 * c8) ^ z)];
+            y[q] = src[(q * 128 + row) * units + ((2 * c8 + 1) ^ z)];
+          }
+        }
+        float v[8] = {x[0].x, x[0].y, x[0].z, x[0].w, y[0].x, y[0].y, y[0].z, y[0].w};
+#pragma unroll
+        for (uint32_t q = 1; q < S; ++q) {
+          v[0] += x[q].x; v[1] += x[q].y; v[2] += x[q].z; v[3] += x[q].w;
+          v[4] += y[q].x; v[5] += y[q].y; v[6] += y[q].z; v[7] += y[q].w;
+        }
+        finish8(v, p.epi, orow, ocol);
+      }
+    };
+    switch (p.split) {
+      case 1: finish(std::integral_constant<uint32_t, 1>{}); break;
+      case 2: finish(std::integral_constant<uint32_t, 2>{}); break;
+      case 4: finish(std::integral_constant<uint32_t, 4>{}); break;
+      default: finish(std::integral_constant<uint32_t, 8>{}); break;
+    }
   }
-  if (p.split > 1)
-    cluster_sync_all();
-  else
-    __syncthreads();
+  __syncthreads();
   if (warp == 5) {
     tc_fence_after();
     tmem_dealloc(tmem, kTmemCols);
-  }
-
-  // Epilogue: this block's share of the tile's 16-byte output pieces.
-  constexpr int kPerRow = kTileCols / 8;
-  constexpr unsigned kUnits = kTileRows * kPerRow;
-  const unsigned u0 = kUnits * rank / (unsigned)p.split;
-  const unsigned u1 = kUnits * (rank + 1) / (unsigned)p.split;
-  const long long row0 = SWAP ? b0 : a0, col0 = SWAP ? a0 : b0;
-  for (unsigned u = u0 + threadIdx.x; u < u1; u += kTileThreads) {
-    const int r = (int)(u / kPerRow), c = 8 * (int)(u % kPerRow);
-    if (row0 + r >= p.rows || col0 + c >= p.cols) continue;
-    const float* src = &tile[r * kLd + c];
-    float v[8];
-    if (p.split > 1) {
-#pragma unroll
-      for (int i = 0; i < 8; ++i) v[i] = 0.f;
-      for (int q = 0; q < p.split; ++q) {  // in rank order: the same sums every time
-        const uint32_t a = smem_cluster_addr(src, (uint32_t)q);
-        const float4 x = ld_cluster_f4(a), y = ld_cluster_f4(a + 16);
-        v[0] += x.x; v[1] += x.y; v[2] += x.z; v[3] += x.w;
-        v[4] += y.x; v[5] += y.y; v[6] += y.z; v[7] += y.w;
-      }
-    } else {
-      const float4 x = *reinterpret_cast<const float4*>(src);
-      const float4 y = *reinterpret_cast<const float4*>(src + 4);
-      v[0] = x.x; v[1] = x.y; v[2] = x.z; v[3] = x.w;
-      v[4] = y.x; v[5] = y.y; v[6] = y.z; v[7] = y.w;
-    }
-    finish8(v, p.epi, row0 + r, col0 + c);
-  }
-  // no block of the cluster leaves while another reads its tile
-  if (p.split > 1) {
-    __syncwarp();
-    cluster_sync_all();
   }
 }
 
