@@ -85,49 +85,44 @@ for _name, (_res, _args) in SIGS.items():
     _fn.restype = _res
 
 
-class _On:
-    """The device and stream of one call. Entered, they are current, so that what the call
-    allocates belongs to the stream that it runs on."""
+_current_device = torch._C._cuda_getDevice
+_current_stream = torch._C._cuda_getCurrentRawStream
 
-    def __init__(self, device, stream):
-        self.device, self.stream, self.undo = device, stream, []
 
-    def __enter__(self):
-        if self.device.index != torch.cuda.current_device():
-            self.undo.append(torch.cuda.device(self.device))
-            self.undo[-1].__enter__()
-        if self.stream is None:
-            return torch.cuda.current_stream().cuda_stream
-        if self.stream.device != self.device:
-            self.__exit__()
-            raise ValueError("the stream is on another device than the tensors")
-        self.undo.append(torch.cuda.stream(self.stream))
-        self.undo[-1].__enter__()
-        return self.stream.cuda_stream
-
-    def __exit__(self, *exc):
-        while self.undo:
-            self.undo.pop().__exit__(None, None, None)
-        return False
+def _on(dev, stream, call):
+    """call(stream handle) with the device and the stream current, so that what it allocates
+    belongs to the stream that it runs on. (The usual case, no stream given and the
+    tensors' device already current, takes no context manager: they cost more than a small
+    call's kernels.)"""
+    if stream is None:
+        if dev == _current_device():
+            return call(_current_stream(dev))
+        with torch.cuda.device(dev):
+            return call(_current_stream(dev))
+    if stream.device_index != dev:
+        raise ValueError("the stream is on another device than the tensors")
+    with torch.cuda.device(dev), torch.cuda.stream(stream):
+        return call(stream.cuda_stream)
 
 
 def _p(t):
     return None if t is None else t.data_ptr()
 
 
-def _matrix(name, t, like, cols=None):
-    """(rows, columns, row stride) of a bf16 matrix: 2-d with neighbouring columns, or any
-    contiguous tensor seen as [rows, last dimension]."""
-    if t.dtype != torch.bfloat16 or t.device != like.device or not t.is_cuda:
+def _matrix(name, t, dev, cols=None):
+    """(rows, columns, row stride) of a bf16 matrix on device `dev`: 2-d with neighbouring
+    columns, or any contiguous tensor seen as [rows, last dimension]."""
+    if t.dtype is not torch.bfloat16 or t.get_device() != dev or dev < 0:
         raise ValueError(f"{name} must be a bf16 tensor on the CUDA device of x")
-    if t.dim() == 2 and (t.shape[1] <= 1 or t.stride(1) == 1):
-        r, c = t.shape
+    shape = t.shape
+    if len(shape) == 2 and (shape[1] <= 1 or t.stride(1) == 1):
+        r, c = shape
         # one row has no stride to keep to; repeated rows (stride 0) are no matrix in memory
         ld = t.stride(0) if r > 1 else c
         if ld < c:
             raise ValueError(f"{name} must not have overlapping rows")
-    elif t.dim() >= 1 and t.is_contiguous():
-        c = t.shape[-1]
+    elif len(shape) >= 1 and t.is_contiguous():
+        c = shape[-1]
         r, ld = (t.numel() // c if c else 0), c
     else:
         raise ValueError(f"{name} must be contiguous, or 2-d with contiguous rows")
@@ -136,9 +131,15 @@ def _matrix(name, t, like, cols=None):
     return r, c, ld
 
 
-def _vector(name, t, n, like):
-    if t is not None and (t.dtype != torch.float32 or t.numel() != n or not t.is_contiguous()
-                          or t.device != like.device):
+def _weight(W, dev, K):
+    if W.dim() != 2 or W.shape[0] != K:
+        raise ValueError("W must be [K, N] with K the last dimension of x")
+    return _matrix("W", W, dev)
+
+
+def _vector(name, t, n, dev):
+    if t is not None and (t.dtype is not torch.float32 or t.numel() != n
+                          or t.get_device() != dev or not t.is_contiguous()):
         raise ValueError(f"{name} must be a contiguous fp32 tensor of {n} elements on the device "
                          "of x")
 
@@ -155,9 +156,9 @@ def _options(workspace, stage_events=None):
 
 def _scratch(workspace, size, like):
     if workspace is None:
-        return torch.empty(size, dtype=torch.uint8, device=like.device) if size else None
-    if workspace.device != like.device:
-        raise ValueError("workspace must be on the device of x")
+        return like.new_empty((size,), dtype=torch.uint8) if size else None
+    if workspace.get_device() != like.get_device() or not workspace.is_contiguous():
+        raise ValueError("workspace must be a contiguous tensor on the device of x")
     return workspace
 
 
@@ -167,30 +168,34 @@ def infini_attn_linear(x, W, bias=None, act=ACT_NONE, residual=None, save_preact
     fp32; K and N multiples of 8. Returns y [..., N], and with save_preact (y, x W + bias),
     the second for the gradient of the activation. x, W, residual and out may be slices of
     wider 2-d tensors (row strides a multiple of 8); out may be residual itself."""
-    M, K, ldx = _matrix("x", x, x)
-    _, N, ldw = _matrix("W", W, x)
-    if W.dim() != 2 or W.shape[0] != K:
-        raise ValueError("W must be [K, N] with K the last dimension of x")
-    _vector("bias", bias, N, x)
-    shape = (*x.shape[:-1], N)
-    a = LinearArgs(x=x.data_ptr(), W=W.data_ptr(), bias=_p(bias), ldx=ldx, ldw=ldw, M=M, K=K, N=N,
-                   act=int(act))
+    dev = x.get_device()
+    M, K, ldx = _matrix("x", x, dev)
+    _, N, ldw = _weight(W, dev, K)
+    shape = x.shape[:-1] + (N,)
+    a = LinearArgs(x=x.data_ptr(), W=W.data_ptr(), ldx=ldx, ldw=ldw, M=M, K=K, N=N, act=act)
+    if bias is not None:
+        _vector("bias", bias, N, dev)
+        a.bias = bias.data_ptr()
     if residual is not None:
         if residual.shape != shape:
             raise ValueError(f"residual must be {shape}")
-        a.residual, a.ldr = residual.data_ptr(), _matrix("residual", residual, x)[2]
-    if out is not None and out.shape != shape:
-        raise ValueError(f"out must be {shape}")
-    with _On(x.device, stream) as s:
-        if out is None:
-            out = torch.empty(shape, dtype=torch.bfloat16, device=x.device)
-        a.y, a.ldy = out.data_ptr(), _matrix("out", out, x)[2]
+        a.residual, a.ldr = residual.data_ptr(), _matrix("residual", residual, dev)[2]
+    if out is not None:
+        if out.shape != shape:
+            raise ValueError(f"out must be {shape}")
+        a.ldy = _matrix("out", out, dev)[2]
+
+    def call(s):
+        y = x.new_empty(shape) if out is None else out
+        a.y = y.data_ptr()
         preact = None
         if save_preact:
-            preact = torch.empty(shape, dtype=torch.bfloat16, device=x.device)
+            preact = x.new_empty(shape)
             a.preact = preact.data_ptr()
         _check(_lib.infini_attn_linear(ctypes.byref(a), s))
-    return (out, preact) if save_preact else out
+        return (y, preact) if save_preact else y
+
+    return _on(dev, stream, call)
 
 
 def infini_attn_linear_backward(x, W, dy, act=ACT_NONE, preact=None, x_grad=True, W_grad=True,
@@ -199,77 +204,86 @@ def infini_attn_linear_backward(x, W, dy, act=ACT_NONE, preact=None, x_grad=True
     ACT_NONE, the forward's preact. dx and dW are bf16 like x and W, dbias [N] fp32; what is
     not asked for is None. The residual's gradient is dy. workspace: optional uint8 CUDA tensor of
     at least linear_backward_workspace_size(...) bytes."""
-    M, K, ldx = _matrix("x", x, x)
-    _, N, ldw = _matrix("W", W, x)
-    if W.dim() != 2 or W.shape[0] != K:
-        raise ValueError("W must be [K, N] with K the last dimension of x")
-    shape = (*x.shape[:-1], N)
+    dev = x.get_device()
+    M, K, ldx = _matrix("x", x, dev)
+    _, N, ldw = _weight(W, dev, K)
+    shape = x.shape[:-1] + (N,)
     if dy.shape != shape:
         raise ValueError(f"dy must be {shape}")
     a = LinearGradArgs(x=x.data_ptr(), W=W.data_ptr(), dy=dy.data_ptr(), ldx=ldx, ldw=ldw,
-                       lddy=_matrix("dy", dy, x)[2], M=M, K=K, N=N, act=int(act))
-    if int(act) != ACT_NONE:
+                       lddy=_matrix("dy", dy, dev)[2], M=M, K=K, N=N, act=act)
+    if act != ACT_NONE:
         if preact is None or preact.shape != shape:
             raise ValueError(f"preact must be {shape}")
-        a.preact, a.ldp = preact.data_ptr(), _matrix("preact", preact, x)[2]
-    dx = dW = dbias = None
-    with _On(x.device, stream) as s:
+        a.preact, a.ldp = preact.data_ptr(), _matrix("preact", preact, dev)[2]
+    if not (x_grad or W_grad or bias_grad):
+        return None, None, None
+
+    def call(s):
+        dx = dW = dbias = None
         if x_grad:
-            dx = torch.empty(x.shape, dtype=x.dtype, device=x.device)
+            dx = x.new_empty(x.shape)
             a.dx = dx.data_ptr()
         if W_grad:
-            dW = torch.empty(W.shape, dtype=W.dtype, device=x.device)
+            dW = W.new_empty((K, N))
             a.dW = dW.data_ptr()
         if bias_grad:
-            dbias = torch.empty((N,), dtype=torch.float32, device=x.device)
+            dbias = x.new_empty((N,), dtype=torch.float32)
             a.dbias = dbias.data_ptr()
-        if dx is None and dW is None and dbias is None:
-            return dx, dW, dbias
         ws = _scratch(workspace, linear_backward_workspace_size(M, K, N, act), x)
         _check(_lib.infini_attn_linear_backward(ctypes.byref(a),
                                                 ctypes.byref(_options(ws, stage_events)), s))
-    return dx, dW, dbias
+        return dx, dW, dbias
+
+    return _on(dev, stream, call)
 
 
 def linear_backward_workspace_size(M, K, N, act=ACT_NONE) -> int:
     return int(_lib.infini_attn_linear_backward_workspace_size(M, K, N, int(act)))
 
 
-def _rows(name, t, like):
-    if t is not None and (t.shape != like.shape or t.dtype != like.dtype
-                          or t.device != like.device or not t.is_contiguous()):
+def _rows(name, t, x):
+    if t is not None and (t.shape != x.shape or t.dtype is not x.dtype
+                          or t.get_device() != x.get_device() or not t.is_contiguous()):
         raise ValueError(f"{name} must be a contiguous CUDA tensor shaped and typed like x")
 
 
 def _norm_args(x, b, gate, alpha, post_weight, post_bias, pre_weight, pre_bias, kind, eps):
-    if x.dim() < 1 or not x.is_cuda or not x.is_contiguous() or x.dtype not in (torch.bfloat16,
-                                                                                torch.float32):
+    dev, shape, dtype = x.get_device(), x.shape, x.dtype
+    if dev < 0 or len(shape) < 1 or not x.is_contiguous() or (dtype is not torch.bfloat16
+                                                              and dtype is not torch.float32):
         raise ValueError("x must be a contiguous bf16 or fp32 CUDA tensor [..., dim]")
-    D = x.shape[-1]
+    D = shape[-1]
     rows = x.numel() // D if D else 0
-    _rows("b", b, x)
-    for name, t in (("post_weight", post_weight), ("post_bias", post_bias),
-                    ("pre_weight", pre_weight), ("pre_bias", pre_bias)):
-        if t is not None:
-            _vector(name, t, D, x)
-    if b is None and (gate is not None or post_weight is not None):
+    a = ResidualNormArgs(x=x.data_ptr(), rows=rows, dim=D, kind=kind, alpha=alpha, eps=eps,
+                         dtype=DTYPE_BF16 if dtype is torch.bfloat16 else DTYPE_F32)
+    if b is not None:
+        _rows("b", b, x)
+        a.b = b.data_ptr()
+    elif gate is not None or post_weight is not None:
         raise ValueError("a gate or a post norm needs b")
-    if (pre_bias is not None and pre_weight is None) or (post_bias is not None
-                                                         and post_weight is None):
-        raise ValueError("a norm's bias needs its weight")
-    groups = 0
+    if pre_weight is not None:
+        _vector("pre_weight", pre_weight, D, dev)
+        a.pre_weight = pre_weight.data_ptr()
+    if post_weight is not None:
+        _vector("post_weight", post_weight, D, dev)
+        a.post_weight = post_weight.data_ptr()
+    if pre_bias is not None or post_bias is not None:
+        if (pre_bias is not None and pre_weight is None) or (post_bias is not None
+                                                             and post_weight is None):
+            raise ValueError("a norm's bias needs its weight")
+        _vector("pre_bias", pre_bias, D, dev)
+        _vector("post_bias", post_bias, D, dev)
+        a.pre_bias, a.post_bias = _p(pre_bias), _p(post_bias)
     if gate is not None:
         if gate.dim() not in (1, 2) or gate.shape[-1] != D or gate.shape[0] == 0:
             raise ValueError("gate must be [dim] or [groups, dim]")
         groups = gate.shape[0] if gate.dim() == 2 else 1
         if rows % groups:
             raise ValueError("gate's groups must divide the rows")
-        _vector("gate", gate, groups * D, x)
-    return ResidualNormArgs(
-        x=x.data_ptr(), b=_p(b), gate=_p(gate), post_weight=_p(post_weight),
-        post_bias=_p(post_bias), pre_weight=_p(pre_weight), pre_bias=_p(pre_bias), rows=rows,
-        gate_groups=groups, dim=D, kind=int(kind),
-        dtype=DTYPE_BF16 if x.dtype == torch.bfloat16 else DTYPE_F32, alpha=alpha, eps=eps)
+        _vector("gate", gate, groups * D, dev)
+        a.gate, a.gate_groups = gate.data_ptr(), groups
+    return a
 
 
 def infini_attn_residual_norm(x, b=None, gate=None, alpha=1.0, post_weight=None, post_bias=None,
@@ -282,15 +296,18 @@ def infini_attn_residual_norm(x, b=None, gate=None, alpha=1.0, post_weight=None,
     a = _norm_args(x, b, gate, alpha, post_weight, post_bias, pre_weight, pre_bias, kind, eps)
     _rows("r_out", r_out, x)
     _rows("h_out", h_out, x)
-    with _On(x.device, stream) as s:
-        r = torch.empty_like(x) if r_out is None else r_out
+
+    def call(s):
+        r = x.new_empty(x.shape) if r_out is None else r_out
         a.r = r.data_ptr()
         h = None
         if pre_weight is not None:
-            h = torch.empty_like(x) if h_out is None else h_out
+            h = x.new_empty(x.shape) if h_out is None else h_out
             a.h = h.data_ptr()
         _check(_lib.infini_attn_residual_norm(ctypes.byref(a), s))
-    return r, h
+        return r, h
+
+    return _on(x.get_device(), stream, call)
 
 
 ResidualNormGrads = namedtuple("ResidualNormGrads",
@@ -302,7 +319,8 @@ def infini_attn_residual_norm_backward(x, b, dr, dh, gate=None, alpha=1.0, post_
                                        kind=NORM_RMS, eps=1e-5, workspace=None, stream=None):
     """Gradient of infini_attn_residual_norm from its inputs and the gradients dr and dh of
     its outputs (either may be None: zero): a ResidualNormGrads with a gradient for every
-    input that was given, None for the others."""
+    input that was given, None for the others. (The vectors' gradients are rows of one
+    tensor.)"""
     a = _norm_args(x, b, gate, alpha, post_weight, post_bias, pre_weight, pre_bias, kind, eps)
     if dr is None and dh is None:
         raise ValueError("dr or dh must be given")
@@ -310,16 +328,30 @@ def infini_attn_residual_norm_backward(x, b, dr, dh, gate=None, alpha=1.0, post_
         raise ValueError("dh needs pre_weight")
     _rows("dr", dr, x)
     _rows("dh", dh, x)
-    with _On(x.device, stream) as s:
-        given = dict(dx=x, db=b, dgate=gate, dpost_weight=post_weight, dpost_bias=post_bias,
-                     dpre_weight=pre_weight, dpre_bias=pre_bias)
-        out = {n: None if t is None else torch.empty_like(t) for n, t in given.items()}
-        g = ResidualNormGradArgs(dr=_p(dr), dh=_p(dh), **{n: _p(t) for n, t in out.items()})
+
+    def call(s):
+        dx = x.new_empty(x.shape)
+        g = ResidualNormGradArgs(dr=_p(dr), dh=_p(dh), dx=dx.data_ptr())
+        db = dgate = None
+        if b is not None:
+            db = x.new_empty(x.shape)
+            g.db = db.data_ptr()
+        if gate is not None:
+            dgate = gate.new_empty(gate.shape)
+            g.dgate = dgate.data_ptr()
+        vectors = [post_weight, post_bias, pre_weight, pre_bias]
+        given = sum(t is not None for t in vectors)
+        if given:
+            rows = iter(x.new_empty((given, a.dim), dtype=torch.float32).unbind(0))
+            vectors = [None if t is None else next(rows).view(t.shape) for t in vectors]
+            g.dpost_weight, g.dpost_bias, g.dpre_weight, g.dpre_bias = map(_p, vectors)
         ws = _scratch(workspace, residual_norm_backward_workspace_size(
             a.rows, a.dim, a.gate_groups, kind), x)
         _check(_lib.infini_attn_residual_norm_backward(ctypes.byref(a), ctypes.byref(g),
                                                        ctypes.byref(_options(ws)), s))
-    return ResidualNormGrads(**out)
+        return ResidualNormGrads(dx, db, dgate, *vectors)
+
+    return _on(x.get_device(), stream, call)
 
 
 def residual_norm_backward_workspace_size(rows, dim, gate_groups=0, kind=NORM_RMS) -> int:
@@ -330,32 +362,38 @@ def residual_norm_backward_workspace_size(rows, dim, gate_groups=0, kind=NORM_RM
 def infini_attn_norm(x, weight, bias=None, kind=NORM_RMS, eps=1e-5, out=None, stream=None):
     """h = norm(x; weight, bias) over the last dimension; x bf16 or fp32, weight and bias
     fp32. out may be x itself."""
-    a = _norm_args(x, None, None, 1.0, None, None, weight, bias, kind, eps)
     if weight is None:
         raise ValueError("weight must be given")
+    a = _norm_args(x, None, None, 1.0, None, None, weight, bias, kind, eps)
     _rows("out", out, x)
-    with _On(x.device, stream) as s:
-        h = torch.empty_like(x) if out is None else out
+
+    def call(s):
+        h = x.new_empty(x.shape) if out is None else out
         _check(_lib.infini_attn_norm(a.x, a.pre_weight, a.pre_bias, h.data_ptr(), a.rows, a.dim,
                                      a.kind, a.dtype, eps, s))
-    return h
+        return h
+
+    return _on(x.get_device(), stream, call)
 
 
 def infini_attn_norm_backward(x, weight, dh, bias=None, kind=NORM_RMS, eps=1e-5, workspace=None,
                               stream=None):
     """Gradient of infini_attn_norm: (dx, dweight, dbias), dbias None without a bias."""
-    a = _norm_args(x, None, None, 1.0, None, None, weight, bias, kind, eps)
     if weight is None or dh is None:
         raise ValueError("weight and dh must be given")
+    a = _norm_args(x, None, None, 1.0, None, None, weight, bias, kind, eps)
     _rows("dh", dh, x)
-    with _On(x.device, stream) as s:
-        dx, dw = torch.empty_like(x), torch.empty_like(weight)
-        dbias = None if bias is None else torch.empty_like(bias)
+
+    def call(s):
+        dx, dw = x.new_empty(x.shape), weight.new_empty(weight.shape)
+        dbias = None if bias is None else bias.new_empty(bias.shape)
         ws = _scratch(workspace, residual_norm_backward_workspace_size(a.rows, a.dim, 0, kind), x)
         _check(_lib.infini_attn_norm_backward(a.x, a.pre_weight, dh.data_ptr(), dx.data_ptr(),
                                               dw.data_ptr(), _p(dbias), a.rows, a.dim, a.kind,
                                               a.dtype, eps, ctypes.byref(_options(ws)), s))
-    return dx, dw, dbias
+        return dx, dw, dbias
+
+    return _on(x.get_device(), stream, call)
 
 
 def infini_attn_block_forward(x, Wq, Wk, Wv, Wo, beta, N, mode, H, W_up, W_down, attn_norm,
@@ -370,7 +408,7 @@ def infini_attn_block_forward(x, Wq, Wk, Wv, Wo, beta, N, mode, H, W_up, W_down,
     gate) + alpha (.). Gates are [D_model] or [groups, D_model] fp32, norms' weights and
     biases [D_model] fp32, b_up and b_down fp32. Returns (y, M_out, z_out) with the layer's
     state (None when state_out is False)."""
-    H_kv = H if H_kv is None else H_kv
+    H_kv, dev = H if H_kv is None else H_kv, x.get_device()
     if x.dim() != 3 or x.dtype != torch.bfloat16 or not x.is_cuda or not x.is_contiguous():
         raise ValueError("x must be a contiguous bf16 CUDA tensor [B, L, D_model]")
     B, L, D = x.shape
@@ -390,25 +428,26 @@ def infini_attn_block_forward(x, Wq, Wk, Wv, Wo, beta, N, mode, H, W_up, W_down,
             if t.dim() not in (1, 2) or groups not in (0, n):
                 raise ValueError("gates must be [D_model] or [groups, D_model], both alike")
             groups = n
-            _vector(name, t, n * D, x)
+            _vector(name, t, n * D, dev)
     vectors = dict(attn_norm=attn_norm, attn_norm_bias=attn_norm_bias,
                    attn_post_norm=attn_post_norm, attn_post_norm_bias=attn_post_norm_bias,
                    mlp_norm=mlp_norm, mlp_norm_bias=mlp_norm_bias, mlp_post_norm=mlp_post_norm,
                    mlp_post_norm_bias=mlp_post_norm_bias)
     for name, t in vectors.items():
-        _vector(name, t, D, x)
-    _vector("b_up", b_up, D_ff, x)
-    _vector("b_down", b_down, D, x)
-    _vector("beta", beta, H, x)
-    _vector("M_in", M_in, B * H_kv * d * d, x)
-    _vector("z_in", z_in, B * H_kv * d, x)
+        _vector(name, t, D, dev)
+    _vector("b_up", b_up, D_ff, dev)
+    _vector("b_down", b_down, D, dev)
+    _vector("beta", beta, H, dev)
+    _vector("M_in", M_in, B * H_kv * d * d, dev)
+    _vector("z_in", z_in, B * H_kv * d, dev)
     _rows("out", out, x)
-    with _On(x.device, stream) as s:
-        y = torch.empty_like(x) if out is None else out
+
+    def call(s):
+        y = x.new_empty(x.shape) if out is None else out
         M_out = z_out = None
         if state_out:
-            M_out = torch.empty((B, H_kv, d, d), device=x.device, dtype=torch.float32)
-            z_out = torch.empty((B, H_kv, d), device=x.device, dtype=torch.float32)
+            M_out = x.new_empty((B, H_kv, d, d), dtype=torch.float32)
+            z_out = x.new_empty((B, H_kv, d), dtype=torch.float32)
         a = BlockArgs(x=x.data_ptr(), Wq=Wq.data_ptr(), Wk=Wk.data_ptr(), Wv=Wv.data_ptr(),
                       Wo=Wo.data_ptr(), beta=beta.data_ptr(), M_in=_p(M_in), z_in=_p(z_in),
                       M_out=_p(M_out), z_out=_p(z_out), attn_gate=_p(attn_gate),
@@ -420,7 +459,9 @@ def infini_attn_block_forward(x, Wq, Wk, Wv, Wo, beta, N, mode, H, W_up, W_down,
         ws = _scratch(workspace, block_workspace_size(B, L, D, D_ff, H, H_kv, N, d, mode), x)
         _check(_lib.infini_attn_block_forward(ctypes.byref(a),
                                               ctypes.byref(_options(ws, stage_events)), s))
-    return y, M_out, z_out
+        return y, M_out, z_out
+
+    return _on(dev, stream, call)
 
 
 def block_workspace_size(B, L, D_model, D_ff, H, H_kv, N, d=128, mode=LINEAR) -> int:

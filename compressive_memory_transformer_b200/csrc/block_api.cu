@@ -100,6 +100,9 @@ int prepare(int* sms) {
 // B200's without one.
 int query_sms() {
   int dev = 0, n = 0;
+  if (cudaGetDevice(&dev) == cudaSuccess && dev >= 0 && dev < kMaxDevices &&
+      (n = g_sms[dev].load(std::memory_order_acquire)) > 0)
+    return n;
   if (cudaGetDevice(&dev) != cudaSuccess ||
       cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || n < 1) {
     cudaGetLastError();
@@ -184,7 +187,7 @@ GradPlan grad_plan(long long M, int K, int N, int act, bool dbias, bool dx, bool
   memset(&f, 0, sizeof(f));
   f.chunks = act_grad_chunks(M, N, sms);
   if (act != INFINI_ACT_NONE) f.dpre = up256((size_t)M * N * 2);
-  if (dbias) f.part = up256((size_t)f.chunks * N * 4);
+  if (dbias && f.chunks > 1) f.part = up256((size_t)f.chunks * N * 4);
   const size_t a = dx ? linear_gemm_scratch(M, K, N, true, sms) : 0;
   const size_t b = dW ? linear_gemm_scratch(K, N, M, true, sms) : 0;
   f.gemm = up256(a > b ? a : b);
@@ -231,14 +234,15 @@ int linear_backward_impl(const infini_attn_linear_grad_t* p, const infini_attn_o
   char* base = static_cast<char*>(sc.ptr);
   const bf16* dy = static_cast<const bf16*>(p->dy);
   bf16* dpre = act ? reinterpret_cast<bf16*>(base) : nullptr;
-  float* part = p->dbias ? reinterpret_cast<float*>(base + f.dpre) : nullptr;
+  // one chunk's sums are dbias itself
+  float* part = f.part ? reinterpret_cast<float*>(base + f.dpre) : p->dbias;
   void* gemm = f.gemm ? base + f.dpre + f.part : nullptr;
   record(opts, 0, stream);
   if (dpre || part) {
     if (act_grad_launch(dy, lddy, static_cast<const bf16*>(p->preact), ldp, p->act, dpre, part,
                         f.chunks, p->M, p->N, stream) != cudaSuccess)
       return INFINI_ERR_CUDA;
-    if (part) {
+    if (f.part) {
       ColsumArgs c;
       memset(&c, 0, sizeof(c));
       c.part = part;

@@ -995,32 +995,37 @@ cudaError_t linear_gemm_launch(const GemmArgs& g, void* scratch, int sms, cudaSt
 
 namespace {
 
-constexpr int kActCols = 256;  // columns of a block: 32 lanes x 8
-constexpr int kActWarps = 8;
+constexpr int kActThreads = 256;
 constexpr int kBatch = 4;
-constexpr int kActBlocks = 3;  // resident per SM
+constexpr int kActBlocks = 3;      // resident per SM
+constexpr int kActNarrowRows = 1024;
+
+// Columns of a block: 256 (a warp per row), or 32 for few rows (64 rows at a time), where
+// one block then takes all of them and the column sums need no second launch.
+constexpr int act_cols(long long M) { return M <= kActNarrowRows ? 32 : 256; }
 
 // dpre = dy act'(pre), one 16-byte piece of a row per thread and step, and the column
 // sums of dpre before its rounding (fp32, one row of `part` per row chunk). HBM-bound:
 // dy and pre read once, dpre written once.
-template <int ACT>
-__global__ void __launch_bounds__(32 * kActWarps, kActBlocks)
+template <int ACT, int COLS>
+__global__ void __launch_bounds__(kActThreads, kActBlocks)
 act_grad_kernel(const __nv_bfloat16* __restrict__ dy, long long lddy,
                 const __nv_bfloat16* __restrict__ pre, long long ldp,
                 __nv_bfloat16* __restrict__ dpre, float* __restrict__ part, long long M, int N) {
-  __shared__ float sums[kActWarps][kActCols];
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int col = blockIdx.x * kActCols + 8 * lane;
+  constexpr int kLanes = COLS / 8, kRows = kActThreads / kLanes;  // rows at a time
+  __shared__ float sums[kRows][COLS];
+  const int lane = threadIdx.x % kLanes, row = threadIdx.x / kLanes;
+  const int col = blockIdx.x * COLS + 8 * lane;
   const bool in = col < N;
   const long long r0 = M * blockIdx.y / gridDim.y, r1 = M * (blockIdx.y + 1) / gridDim.y;
   float s[8] = {};
   if (in) {
     // kBatch rows' loads in flight before the first is used
-    for (long long r = r0 + warp; r < r1; r += kBatch * kActWarps) {
+    for (long long r = r0 + row; r < r1; r += kBatch * kRows) {
       uint4 g[kBatch], z[kBatch];
 #pragma unroll
       for (int k = 0; k < kBatch; ++k) {
-        const long long rk = r + k * kActWarps;
+        const long long rk = r + k * kRows;
         if (rk < r1) {
           g[k] = __ldcs(reinterpret_cast<const uint4*>(dy + rk * lddy + col));
           if (ACT != kActNone) z[k] = __ldcs(reinterpret_cast<const uint4*>(pre + rk * ldp + col));
@@ -1028,7 +1033,7 @@ act_grad_kernel(const __nv_bfloat16* __restrict__ dy, long long lddy,
       }
 #pragma unroll
       for (int k = 0; k < kBatch; ++k) {
-        const long long rk = r + k * kActWarps;
+        const long long rk = r + k * kRows;
         if (rk >= r1) break;
         const uint32_t gw[4] = {g[k].x, g[k].y, g[k].z, g[k].w};
         const uint32_t zw[4] = {z[k].x, z[k].y, z[k].z, z[k].w};
@@ -1054,13 +1059,13 @@ act_grad_kernel(const __nv_bfloat16* __restrict__ dy, long long lddy,
   }
   if (!part) return;
 #pragma unroll
-  for (int i = 0; i < 8; ++i) sums[warp][8 * lane + i] = s[i];
+  for (int i = 0; i < 8; ++i) sums[row][8 * lane + i] = s[i];
   __syncthreads();
-  const int c = blockIdx.x * kActCols + threadIdx.x;
-  if (c < N) {
+  const int c = blockIdx.x * COLS + threadIdx.x;
+  if (threadIdx.x < COLS && c < N) {
     float v = 0.f;
-#pragma unroll
-    for (int w = 0; w < kActWarps; ++w) v += sums[w][threadIdx.x];
+#pragma unroll 8
+    for (int w = 0; w < kRows; ++w) v += sums[w][threadIdx.x];
     part[(long long)blockIdx.y * N + c] = v;
   }
 }
@@ -1087,30 +1092,41 @@ __global__ void __launch_bounds__(256) colsum_kernel(const ColsumArgs a) {
 }  // namespace
 
 int act_grad_chunks(long long M, int N, int sms) {
+  if (M <= kActNarrowRows) return 1;
   // one wave of resident blocks, one batch of rows per warp at least
-  const long long across = (N + kActCols - 1) / kActCols;
+  const long long across = (N + act_cols(M) - 1) / act_cols(M);
   long long c = (long long)kActBlocks * sms / across;
-  const long long most = (M + kBatch * kActWarps - 1) / (kBatch * kActWarps);
+  const long long most = (M + 8 * kBatch - 1) / (8 * kBatch);
   c = c < most ? c : most;
   return (int)(c < 1 ? 1 : (c > 65535 ? 65535 : c));
 }
 
+namespace {
+template <int ACT>
+void act_grad(const dim3& grid, const __nv_bfloat16* dy, long long lddy, const __nv_bfloat16* pre,
+              long long ldp, __nv_bfloat16* dpre, float* part, long long M, int N,
+              cudaStream_t stream) {
+  if (act_cols(M) == 32)
+    act_grad_kernel<ACT, 32><<<grid, kActThreads, 0, stream>>>(dy, lddy, pre, ldp, dpre, part, M,
+                                                              N);
+  else
+    act_grad_kernel<ACT, 256><<<grid, kActThreads, 0, stream>>>(dy, lddy, pre, ldp, dpre, part, M,
+                                                               N);
+}
+}  // namespace
+
 cudaError_t act_grad_launch(const __nv_bfloat16* dy, long long lddy, const __nv_bfloat16* pre,
                             long long ldp, int act, __nv_bfloat16* dpre, float* part, int chunks,
                             long long M, int N, cudaStream_t stream) {
-  const dim3 grid((unsigned)((N + kActCols - 1) / kActCols), (unsigned)chunks);
+  const dim3 grid((unsigned)((N + act_cols(M) - 1) / act_cols(M)), (unsigned)chunks);
   switch (act) {
-#define INFINI_ACT_CASE(A)                                                                     \
-  case A:                                                                                      \
-    act_grad_kernel<A><<<grid, 32 * kActWarps, 0, stream>>>(dy, lddy, pre, ldp, dpre, part, M, \
-                                                            N);                                \
-    break;
-    INFINI_ACT_CASE(kActNone)
-    INFINI_ACT_CASE(kActRelu)
-    INFINI_ACT_CASE(kActSilu)
-    INFINI_ACT_CASE(kActGelu)
-    INFINI_ACT_CASE(kActGeluTanh)
-#undef INFINI_ACT_CASE
+    case kActNone: act_grad<kActNone>(grid, dy, lddy, pre, ldp, dpre, part, M, N, stream); break;
+    case kActRelu: act_grad<kActRelu>(grid, dy, lddy, pre, ldp, dpre, part, M, N, stream); break;
+    case kActSilu: act_grad<kActSilu>(grid, dy, lddy, pre, ldp, dpre, part, M, N, stream); break;
+    case kActGelu: act_grad<kActGelu>(grid, dy, lddy, pre, ldp, dpre, part, M, N, stream); break;
+    case kActGeluTanh:
+      act_grad<kActGeluTanh>(grid, dy, lddy, pre, ldp, dpre, part, M, N, stream);
+      break;
     default: return cudaErrorInvalidValue;
   }
   return cudaGetLastError();
