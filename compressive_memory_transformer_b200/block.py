@@ -222,7 +222,7 @@ def infini_attn_linear_backward(x, W, dy, act=ACT_NONE, preact=None, x_grad=True
     def call(s):
         dx = dW = dbias = None
         if x_grad:
-            dx = x.new_empty(x.shape)
+            dx = x.new_empty(x.shape)  # x may be a slice
             a.dx = dx.data_ptr()
         if W_grad:
             dW = W.new_empty((K, N))
@@ -298,11 +298,11 @@ def infini_attn_residual_norm(x, b=None, gate=None, alpha=1.0, post_weight=None,
     _rows("h_out", h_out, x)
 
     def call(s):
-        r = x.new_empty(x.shape) if r_out is None else r_out
+        r = torch.empty_like(x) if r_out is None else r_out
         a.r = r.data_ptr()
         h = None
         if pre_weight is not None:
-            h = x.new_empty(x.shape) if h_out is None else h_out
+            h = torch.empty_like(x) if h_out is None else h_out
             a.h = h.data_ptr()
         _check(_lib.infini_attn_residual_norm(ctypes.byref(a), s))
         return r, h
@@ -319,8 +319,7 @@ def infini_attn_residual_norm_backward(x, b, dr, dh, gate=None, alpha=1.0, post_
                                        kind=NORM_RMS, eps=1e-5, workspace=None, stream=None):
     """Gradient of infini_attn_residual_norm from its inputs and the gradients dr and dh of
     its outputs (either may be None: zero): a ResidualNormGrads with a gradient for every
-    input that was given, None for the others. (The vectors' gradients are rows of one
-    tensor.)"""
+    input that was given, None for the others."""
     a = _norm_args(x, b, gate, alpha, post_weight, post_bias, pre_weight, pre_bias, kind, eps)
     if dr is None and dh is None:
         raise ValueError("dr or dh must be given")
@@ -330,26 +329,15 @@ def infini_attn_residual_norm_backward(x, b, dr, dh, gate=None, alpha=1.0, post_
     _rows("dh", dh, x)
 
     def call(s):
-        dx = x.new_empty(x.shape)
-        g = ResidualNormGradArgs(dr=_p(dr), dh=_p(dh), dx=dx.data_ptr())
-        db = dgate = None
-        if b is not None:
-            db = x.new_empty(x.shape)
-            g.db = db.data_ptr()
-        if gate is not None:
-            dgate = gate.new_empty(gate.shape)
-            g.dgate = dgate.data_ptr()
-        vectors = [post_weight, post_bias, pre_weight, pre_bias]
-        given = sum(t is not None for t in vectors)
-        if given:
-            rows = iter(x.new_empty((given, a.dim), dtype=torch.float32).unbind(0))
-            vectors = [None if t is None else next(rows).view(t.shape) for t in vectors]
-            g.dpost_weight, g.dpost_bias, g.dpre_weight, g.dpre_bias = map(_p, vectors)
+        out = [None if t is None else torch.empty_like(t)
+               for t in (x, b, gate, post_weight, post_bias, pre_weight, pre_bias)]
+        g = ResidualNormGradArgs(_p(dr), _p(dh), *[None if t is None else t.data_ptr()
+                                                   for t in out])
         ws = _scratch(workspace, residual_norm_backward_workspace_size(
             a.rows, a.dim, a.gate_groups, kind), x)
         _check(_lib.infini_attn_residual_norm_backward(ctypes.byref(a), ctypes.byref(g),
                                                        ctypes.byref(_options(ws)), s))
-        return ResidualNormGrads(dx, db, dgate, *vectors)
+        return ResidualNormGrads(*out)
 
     return _on(x.get_device(), stream, call)
 
@@ -368,7 +356,7 @@ def infini_attn_norm(x, weight, bias=None, kind=NORM_RMS, eps=1e-5, out=None, st
     _rows("out", out, x)
 
     def call(s):
-        h = x.new_empty(x.shape) if out is None else out
+        h = torch.empty_like(x) if out is None else out
         _check(_lib.infini_attn_norm(a.x, a.pre_weight, a.pre_bias, h.data_ptr(), a.rows, a.dim,
                                      a.kind, a.dtype, eps, s))
         return h
@@ -385,8 +373,8 @@ def infini_attn_norm_backward(x, weight, dh, bias=None, kind=NORM_RMS, eps=1e-5,
     _rows("dh", dh, x)
 
     def call(s):
-        dx, dw = x.new_empty(x.shape), weight.new_empty(weight.shape)
-        dbias = None if bias is None else bias.new_empty(bias.shape)
+        dx, dw = torch.empty_like(x), torch.empty_like(weight)
+        dbias = None if bias is None else torch.empty_like(bias)
         ws = _scratch(workspace, residual_norm_backward_workspace_size(a.rows, a.dim, 0, kind), x)
         _check(_lib.infini_attn_norm_backward(a.x, a.pre_weight, dh.data_ptr(), dx.data_ptr(),
                                               dw.data_ptr(), _p(dbias), a.rows, a.dim, a.kind,

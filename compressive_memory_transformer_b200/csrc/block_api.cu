@@ -443,25 +443,31 @@ int residual_norm_backward_impl(const infini_attn_residual_norm_t* p,
     if (norm_backward_launch(a, p->kind, p->dtype == INFINI_DTYPE_F32, f.blocks, stream) !=
         cudaSuccess)
       return INFINI_ERR_CUDA;
-    if (f.gpart && gate_sum_launch(a.gpart, g->dgate, a.groups, f.cpg, p->dim, stream) !=
-                       cudaSuccess)
-      return INFINI_ERR_CUDA;
   } else if (g->dgate && cudaMemsetAsync(g->dgate, 0, nv * (size_t)a.groups, stream) !=
                              cudaSuccess) {
     return INFINI_ERR_CUDA;
   }
-  if (sums) {
+  const bool gates = p->rows > 0 && f.gpart;
+  if (sums || gates) {
     ColsumArgs c;
     memset(&c, 0, sizeof(c));
-    c.part = a.part;
-    c.sets = norm_sets(p->kind);
-    c.out[0] = g->dpre_weight;
-    c.out[1] = g->dpost_weight;
-    if (p->kind == INFINI_NORM_LAYER) {
-      c.out[2] = g->dpre_bias;
-      c.out[3] = g->dpost_bias;
+    if (sums) {
+      c.part = a.part;
+      c.sets = norm_sets(p->kind);
+      c.out[0] = g->dpre_weight;
+      c.out[1] = g->dpost_weight;
+      if (p->kind == INFINI_NORM_LAYER) {
+        c.out[2] = g->dpre_bias;
+        c.out[3] = g->dpost_bias;
+      }
+      c.count = p->rows > 0 ? f.blocks : 0;
     }
-    c.count = p->rows > 0 ? f.blocks : 0;
+    if (gates) {
+      c.gpart = a.gpart;
+      c.dgate = g->dgate;
+      c.groups = a.groups;
+      c.cpg = f.cpg;
+    }
     c.D = p->dim;
     if (colsum_launch(c, stream) != cudaSuccess) return INFINI_ERR_CUDA;
   }

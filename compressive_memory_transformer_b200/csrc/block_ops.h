@@ -43,15 +43,19 @@ cudaError_t act_grad_launch(const __nv_bfloat16* dy, long long lddy, const __nv_
                             long long ldp, int act, __nv_bfloat16* dpre, float* part, int chunks,
                             long long M, int N, cudaStream_t stream);
 
-// out[s][c] = sum over k of part[k][s][c] in a fixed order, for `sets` vectors of D
-// columns; a NULL out[s] is skipped. count = 0 writes zeros.
-constexpr int kMaxSets = 5;
+// Sums of partial vectors of D columns in a fixed order, in one launch:
+//   out[s][c] = sum over k < count of part[k][s][c] (a NULL out[s] is skipped),
+//   dgate[g][c] = sum over k < cpg of gpart[g][k][c] (with gpart).
+// count = 0 writes zeros.
+constexpr int kMaxSets = 4;
 struct ColsumArgs {
   const float* part;
   float* out[kMaxSets];
-  int sets;
+  int sets, D;
   long long count;
-  int D;
+  const float* gpart;
+  float* dgate;
+  long long groups, cpg;
 };
 cudaError_t colsum_launch(const ColsumArgs& a, cudaStream_t stream);
 
@@ -82,8 +86,4 @@ void norm_backward_plan(long long rows, int D, long long groups, int sms, int* b
 constexpr int norm_sets(int kind) { return kind == kNormLayer ? 4 : 2; }
 cudaError_t norm_backward_launch(const NormArgs& a, int kind, bool f32, int blocks,
                                  cudaStream_t stream);
-// dgate[g] = sum over the group's chunks of gpart
-cudaError_t gate_sum_launch(const float* gpart, float* dgate, long long groups, long long cpg,
-                            int D, cudaStream_t stream);
-
 }  // namespace infini

@@ -143,6 +143,13 @@ struct TileParams {
   Epilogue epi;
 };
 
+// What the 16-byte unit of a row of `units` (2, 4, 8 or 16) units is xored with: below
+// units, and different for the rows that share 128 bytes of shared memory with eight
+// neighbours' accesses.
+__device__ __forceinline__ uint32_t recv_swizzle(uint32_t row, uint32_t units) {
+  return units >= 8 ? row & 7u : units == 4 ? (row >> 1) & 3u : (row >> 2) & 1u;
+}
+
 constexpr int kTileThreads = 256;
 constexpr int tile_stages(int bn) { return bn <= 16 ? 10 : bn <= 32 ? 9 : bn <= 64 ? 7 : 5; }
 constexpr int tile_stage_bytes(int bn) { return (128 + bn) * 128; }
@@ -306,7 +313,7 @@ linear_tile_kernel(const __grid_constant__ CUtensorMap tm_a,
           // share of rank q: columns [q BN / S, ..); from rank r: [r][128 rows][BN / S],
           // 16-byte units of a row swizzled
           const uint32_t per = (uint32_t)BN >> log_s, units = per / 4;
-          const uint32_t x = (units >= 8 ? (uint32_t)m : (uint32_t)m >> 1) & (units >= 8 ? 7u : 3u);
+          const uint32_t x = recv_swizzle((uint32_t)m, units);
           if ((long long)a0 + m < p.rows) {
 #pragma unroll
             for (int i = 0; i < 32; i += 4) {
@@ -341,7 +348,7 @@ linear_tile_kernel(const __grid_constant__ CUtensorMap tm_a,
             y[q] = src[(q * per + row) * 32 + 2 * c8 + 1];
           } else {
             constexpr uint32_t units = per / 4;
-            const uint32_t z = (units >= 8 ? row : row >> 1) & (units >= 8 ? 7u : 3u);
+            const uint32_t z = recv_swizzle(row, units);
             x[q] = src[(q * 128 + row) * units + ((2 * c8) ^ z)];
             y[q] = src[(q * 128 + row) * units + ((2 * c8 + 1) ^ z)];
           }
@@ -477,14 +484,20 @@ linear_pair_kernel(const __grid_constant__ CUtensorMap tm_a,
     tma_prefetch_desc(&tm_b);
     tma_prefetch_desc(&io.out);
   }
+  __syncwarp();
+  cluster_arrive();  // barriers initialised in both CTAs before any remote use
   if (warp == kEpiWarps + 1) {
     tmem_alloc_pair(tmem_slot, 512);
     tmem_relinquish_pair();
   }
-  tc_fence_before();
-  cluster_sync_all();  // barriers initialised in both CTAs before any remote use
-  tc_fence_after();
-  const uint32_t tmem = *tmem_slot;
+  cluster_wait();
+  uint32_t tmem = 0;
+  if (warp != kEpiWarps) {  // the copies start without tensor memory
+    tc_fence_before();
+    named_bar_sync(1, kPairThreads - 32);
+    tc_fence_after();
+    tmem = *tmem_slot;
+  }
   bool ok = true;
 
   if (warp == kEpiWarps) {
@@ -719,11 +732,11 @@ linear_pair_kernel(const __grid_constant__ CUtensorMap tm_a,
     }
     if (lane == 0) {
       // residual copies that a given-up wait left behind have landed, and every store has
-      // been done
+      // been read from shared memory
       if (!ok)
         for (int k = loads > mask + 1 ? loads - mask - 1 : 0; k < loads; ++k)
           drain_wait(&rbar[k & mask], (uint32_t)((k >> turns) & 1));
-      tma_store_wait_all();
+      bulk_wait_group_read0();
     }
     __syncwarp();
   }
@@ -900,14 +913,6 @@ cudaError_t tile_launch(const GemmArgs& g, int split, cudaStream_t stream) {
   return e != cudaSuccess ? e : cudaGetLastError();
 }
 
-// Blocks that share one tile's reduction: as many (a power of two, 8 at most) as one wave
-// of blocks has room for, each with two k-steps at least.
-int tile_split(long long tiles, long long ksteps, int sms) {
-  int s = 1;
-  while (s < 8 && tiles * 2 * s <= sms && ksteps >= 4 * s) s *= 2;
-  return s;
-}
-
 template <typename K>
 cudaError_t set_smem(K* kernel, int bytes) {
   return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
@@ -926,6 +931,9 @@ cudaError_t linear_set_attributes() {
   set(linear_tile_kernel<32, true, false, false>, tile_smem(32));
   set(linear_tile_kernel<64, true, true, false>, tile_smem(64));
   set(linear_tile_kernel<64, true, false, false>, tile_smem(64));
+  set(linear_tile_kernel<64, false, false, true>, tile_smem(64));
+  set(linear_tile_kernel<64, false, false, false>, tile_smem(64));
+  set(linear_tile_kernel<64, false, true, true>, tile_smem(64));
   set(linear_tile_kernel<128, false, false, true>, tile_smem(128));
   set(linear_tile_kernel<128, false, false, false>, tile_smem(128));
   set(linear_tile_kernel<128, false, true, true>, tile_smem(128));
@@ -937,27 +945,67 @@ cudaError_t linear_set_attributes() {
 
 namespace {
 
-// How a product is run. TUNE: thresholds from measurements.
+// How a product is run.
 struct GemmPlan {
   bool pair;
+  int bn;     // tile width without a pair
   int split;  // blocks of a cluster, or parts of a pair launch
 };
 
+// Estimated time (us) of the tile kernel: a launch, and for every wave of blocks the time to
+// the first operands, the k-steps, which bring (128 + bn) x 128 bytes into an SM at its
+// share of L2 bandwidth, and the exchange of a split. Measured on 24 shapes from 100 x 512 x
+// 1024 to 16384 x 256 x 512 in all three storage orders; the estimates are within 15% there.
+double tile_time(int bn, int split, long long blocks, long long ksteps, int sms) {
+  static const double step128 = 0.29, step64 = 0.20, step32 = 0.165, step16 = 0.15;
+  static const double swap128[4] = {0.0, 2.3, 3.2, 4.4};  // for 1, 2, 4, 8 blocks
+  const double step = bn >= 128 ? step128 : bn >= 64 ? step64 : bn >= 32 ? step32 : step16;
+  const int i = split == 1 ? 0 : split == 2 ? 1 : split == 4 ? 2 : 3;
+  // clusters of eight find room on fewer SMs
+  const long long room = split == 8 ? sms * 3 / 4 : sms;
+  const double waves = (double)((blocks + room - 1) / room);
+  const double part = (double)((ksteps + split - 1) / split);
+  return 1.8 + waves * (2.8 + part * step + swap128[i] * (0.3 + 0.7 * bn / 128));
+}
+
+// The same for the pair kernel: persistent, a k-step of 256 x 256 in 0.31 us, the last
+// tile's epilogue exposed; a split adds a launch and the partial sums' way through L2.
+double pair_time(long long P, long long Q, int split, long long units, long long ksteps,
+                 int sms) {
+  const long long pairs = sms / 2, part = (ksteps + split - 1) / split;
+  const double waves = (double)((units + pairs - 1) / pairs);
+  double t = 7.2 + waves * (part * 0.31 > 2.5 ? part * 0.31 : 2.5);
+  if (split > 1) t += 3.0 + (double)split * P * Q * 8 / 8e6;
+  return t;
+}
+
+int tile_split(int bn, long long tiles, long long ksteps, int sms) {
+  int best = 1;
+  double t = tile_time(bn, 1, tiles, ksteps, sms);
+  for (int s = 2; s <= 8 && ksteps >= 2 * s; s *= 2) {
+    const double u = tile_time(bn, s, tiles * s, ksteps, sms);
+    if (u < t) t = u, best = s;
+  }
+  return best;
+}
+
+// The fastest by the estimates (scratch: whether a split over pairs is possible).
 GemmPlan gemm_plan(long long P, long long Q, long long R, bool scratch, int sms) {
   const long long ksteps = (R + kKStep - 1) / kKStep;
-  const long long small = (P + 127) / 128 * ((Q + 127) / 128);
   const long long big = (P + 255) / 256 * ((Q + 255) / 256);
-  const int pairs = sms / 2;
-  if (P > 64 && small > sms) {
-    GemmPlan g{true, 1};
-    return g;
+  GemmPlan best{true, 256, 1};
+  double t = pair_time(P, Q, 1, big, ksteps, sms);
+  for (int s = 2; scratch && s <= 8 && ksteps >= 8 * s && big * s <= sms / 2; ++s) {
+    const double u = pair_time(P, Q, s, big * s, ksteps, sms);
+    if (u < t) t = u, best = GemmPlan{true, 256, s};
   }
-  if (P > 64 && scratch && ksteps >= 32 && big * 2 <= pairs && small * 2 > sms / 2) {
-    long long s = pairs / big;
-    while (s > 1 && ksteps / s < 16) --s;
-    if (s > 1) return GemmPlan{true, (int)s};
+  for (int bn = 64; bn <= 128; bn *= 2) {
+    const long long tiles = (P + 127) / 128 * ((Q + bn - 1) / bn);
+    const int s = tile_split(bn, tiles, ksteps, sms);
+    const double u = tile_time(bn, s, tiles * s, ksteps, sms);
+    if (u < t) t = u, best = GemmPlan{false, bn, s};
   }
-  return GemmPlan{false, tile_split(small, ksteps, sms)};
+  return best;
 }
 
 }  // namespace
@@ -971,14 +1019,14 @@ size_t linear_gemm_scratch(long long P, long long Q, long long R, bool scratch, 
 // x^T d (both across).
 cudaError_t linear_gemm_launch(const GemmArgs& g, void* scratch, int sms, cudaStream_t stream) {
   if (g.a_mn && !g.b_mn) return cudaErrorInvalidValue;
-  const long long ksteps = (g.R + kKStep - 1) / kKStep;
   // Few rows, stored along the reduction: the rows take the narrow side of the tile.
   if (g.P <= 64 && !g.a_mn) {
-    const int s = tile_split((g.Q + 127) / 128, ksteps, sms);
-    if (g.P <= 16)
+    const int bn = g.P <= 16 ? 16 : g.P <= 32 ? 32 : 64;
+    const int s = tile_split(bn, (g.Q + 127) / 128, (g.R + kKStep - 1) / kKStep, sms);
+    if (bn == 16)
       return g.b_mn ? tile_launch<16, true, true, false>(g, s, stream)
                     : tile_launch<16, true, false, false>(g, s, stream);
-    if (g.P <= 32)
+    if (bn == 32)
       return g.b_mn ? tile_launch<32, true, true, false>(g, s, stream)
                     : tile_launch<32, true, false, false>(g, s, stream);
     return g.b_mn ? tile_launch<64, true, true, false>(g, s, stream)
@@ -986,6 +1034,10 @@ cudaError_t linear_gemm_launch(const GemmArgs& g, void* scratch, int sms, cudaSt
   }
   const GemmPlan f = gemm_plan(g.P, g.Q, g.R, scratch != nullptr, sms);
   if (f.pair) return pair_launch(g, f.split, static_cast<float*>(scratch), sms, stream);
+  if (f.bn == 64)
+    return g.a_mn   ? tile_launch<64, false, true, true>(g, f.split, stream)
+           : g.b_mn ? tile_launch<64, false, false, true>(g, f.split, stream)
+                    : tile_launch<64, false, false, false>(g, f.split, stream);
   return g.a_mn   ? tile_launch<128, false, true, true>(g, f.split, stream)
          : g.b_mn ? tile_launch<128, false, false, true>(g, f.split, stream)
                   : tile_launch<128, false, false, false>(g, f.split, stream);
@@ -1070,22 +1122,40 @@ act_grad_kernel(const __nv_bfloat16* __restrict__ dy, long long lddy,
   }
 }
 
-// Fixed-order column sums: 32 columns x 8 partial sums of every eighth row.
-__global__ void __launch_bounds__(256) colsum_kernel(const ColsumArgs a) {
+// Fixed-order sums: 32 columns x 8 partial sums of every eighth row. The grid's rows are
+// the sets, then the groups (in layers of gy, a grid axis holding 65535).
+__global__ void __launch_bounds__(256) colsum_kernel(const ColsumArgs a, const unsigned gy) {
   __shared__ float sums[8][33];
-  const int lane = threadIdx.x & 31, w = threadIdx.x >> 5, set = blockIdx.y;
-  if (!a.out[set]) return;
+  const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
+  const float* src;
+  float* dst;
+  long long count, step;
+  if (blockIdx.z == 0 && blockIdx.y < (unsigned)a.sets) {
+    dst = a.out[blockIdx.y];
+    src = a.part + (long long)blockIdx.y * a.D;
+    count = a.count;
+    step = (long long)a.sets * a.D;
+  } else {
+    if (blockIdx.y < (unsigned)a.sets) return;
+    const long long g = (blockIdx.y - (unsigned)a.sets) + (long long)blockIdx.z * gy;
+    if (g >= a.groups) return;
+    dst = a.dgate + g * a.D;
+    src = a.gpart + g * a.cpg * a.D;
+    count = a.cpg;
+    step = a.D;
+  }
+  if (!dst) return;
   const int c = blockIdx.x * 32 + lane;
   float v = 0.f;
   if (c < a.D)
 #pragma unroll 4
-    for (long long k = w; k < a.count; k += 8) v += a.part[(k * a.sets + set) * a.D + c];
+    for (long long k = w; k < count; k += 8) v += src[k * step + c];
   sums[w][lane] = v;
   __syncthreads();
   if (w == 0 && c < a.D) {
 #pragma unroll
     for (int i = 1; i < 8; ++i) v += sums[i][lane];
-    a.out[set][c] = v;
+    dst[c] = v;
   }
 }
 
@@ -1133,7 +1203,12 @@ cudaError_t act_grad_launch(const __nv_bfloat16* dy, long long lddy, const __nv_
 }
 
 cudaError_t colsum_launch(const ColsumArgs& a, cudaStream_t stream) {
-  colsum_kernel<<<dim3((unsigned)((a.D + 31) / 32), (unsigned)a.sets), 256, 0, stream>>>(a);
+  const long long groups = a.gpart ? a.groups : 0;
+  const unsigned gy = (unsigned)(groups < 32768 ? groups : 32768);
+  const long long gz = gy ? (groups + gy - 1) / gy : 1;
+  if (gz > 65535) return cudaErrorInvalidValue;
+  const dim3 grid((unsigned)((a.D + 31) / 32), (unsigned)a.sets + gy, (unsigned)gz);
+  colsum_kernel<<<grid, 256, 0, stream>>>(a, gy);
   return cudaGetLastError();
 }
 

@@ -15,7 +15,7 @@
 // stays the same (dgate = w sum d bn + c sum d; dw_post and dc_post get gate times the
 // sums), the others in shared memory: with them in registers the kernel spilled 0.5 to 1 KB
 // per thread. Each block leaves one row of partial sums per vector, each chunk of a gate
-// group one row of dgate, and colsum / gate_sum add them in a fixed order. The next row is
+// group one row of dgate, and one launch adds them in a fixed order. The next row is
 // asked for in L2 while the present one is worked on.
 #include "norm_common.cuh"
 
@@ -240,25 +240,6 @@ cudaError_t allow() {
   return e;
 }
 
-__global__ void __launch_bounds__(256)
-gate_sum_kernel(const float* __restrict__ gpart, float* __restrict__ dgate, long long cpg, int D) {
-  __shared__ float sums[8][33];
-  const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
-  const int c = blockIdx.x * 32 + lane;
-  const long long g = blockIdx.y + (long long)blockIdx.z * gridDim.y;
-  float v = 0.f;
-  if (c < D)
-#pragma unroll 4
-    for (long long k = w; k < cpg; k += 8) v += gpart[(g * cpg + k) * D + c];
-  sums[w][lane] = v;
-  __syncthreads();
-  if (w == 0 && c < D) {
-#pragma unroll
-    for (int i = 1; i < 8; ++i) v += sums[i][lane];
-    dgate[g * D + c] = v;
-  }
-}
-
 }  // namespace
 
 void norm_backward_plan(long long rows, int D, long long groups, int sms, int* blocks,
@@ -299,23 +280,6 @@ cudaError_t norm_backward_launch(const NormArgs& a, int kind, bool f32, int bloc
                       : launch<float, false, false>(a, blocks, stream);
   return vec ? launch<__nv_bfloat16, true, false>(a, blocks, stream)
              : launch<__nv_bfloat16, false, false>(a, blocks, stream);
-}
-
-cudaError_t gate_sum_launch(const float* gpart, float* dgate, long long groups, long long cpg,
-                            int D, cudaStream_t stream) {
-  // the groups over the grid's second and third axes (65535 rows each)
-  const unsigned gy = (unsigned)(groups < 32768 ? groups : 32768);
-  if (groups % gy) {  // whole layers of gy groups, then the rest
-    const long long head = groups / gy * gy;
-    const cudaError_t e = gate_sum_launch(gpart, dgate, head, cpg, D, stream);
-    if (e != cudaSuccess) return e;
-    return gate_sum_launch(gpart + head * cpg * D, dgate + head * D, groups - head, cpg, D, stream);
-  }
-  const long long gz = groups / gy;
-  if (gz > 65535) return cudaErrorInvalidValue;
-  gate_sum_kernel<<<dim3((unsigned)((D + 31) / 32), gy, (unsigned)gz), 256, 0, stream>>>(
-      gpart, dgate, cpg, D);
-  return cudaGetLastError();
 }
 
 }  // namespace infini
