@@ -83,6 +83,10 @@ __device__ __forceinline__ void st_cluster_f1(uint32_t addr, uint32_t v) {
   asm volatile("st.shared::cluster.b32 [%0], %1;" ::"r"(addr), "r"(v) : "memory");
 }
 
+__device__ __forceinline__ void st_shared_f1(uint32_t addr, uint32_t v) {
+  asm volatile("st.shared.b32 [%0], %1;" ::"r"(addr), "r"(v) : "memory");
+}
+
 // The address in the cluster's window of this block's shared address, in block `rank`.
 __device__ __forceinline__ uint32_t mapa(uint32_t addr, uint32_t rank) {
   uint32_t r;
@@ -143,6 +147,11 @@ struct TileParams {
   Epilogue epi;
 };
 
+// Counts this warp in at a barrier without waiting.
+__device__ __forceinline__ void named_bar_arrive(uint32_t id, uint32_t nthreads) {
+  asm volatile("bar.arrive %0, %1;" ::"r"(id), "r"(nthreads) : "memory");
+}
+
 // What the 16-byte unit of a row of `units` (2, 4, 8 or 16) units is xored with: below
 // units, and different for the rows that share 128 bytes of shared memory with eight
 // neighbours' accesses.
@@ -163,9 +172,10 @@ static_assert(tile_smem(128) <= 232448 && tile_smem(64) <= 232448, "shared memor
 // its columns). The blocks of a cluster split the reduction; each owns an equal share of
 // the tile's columns (rows with SWAP) and gets the others' partial sums of it stored into
 // its shared memory, so that one cluster barrier is all that the exchange takes, and adds
-// them in rank order, the same sums every time. A block alone with !SWAP, whose accumulator
-// lanes are output rows, writes straight from registers; with SWAP the same exchange turns
-// the tile round.
+// them in rank order, the same sums every time. A block alone takes the same way inside its
+// own shared memory: the accumulator's lanes are rows (columns with SWAP) of the output, and
+// writing them out from registers, 16 bytes to each of 32 rows at a time, took 1700 cycles
+// per 128 x 128 tile.
 // Bound by latency when small (the operands' first bytes, one pass through the tensor
 // cores, the exchange) and by the stream of the weights with few rows: every block keeps
 // its whole ring (160 to 180 KB) in flight.
@@ -213,25 +223,26 @@ linear_tile_kernel(const __grid_constant__ CUtensorMap tm_a,
   };
 
   cluster_arrive();  // waited for before the exchange: every block has started by then
+  uint32_t tmem = 0;
   if (warp == 4) {
-    if (lane == 0) {
-      // the first copies are on their way before the block has set up the rest
-      for (int x = 0; x < 2 * ST + 1; ++x) mbar_init(&bars[x], 1);
-      fence_barrier_init();
-      while (issued < ST && ks0 + issued < ks1) load(issued);
-    }
+    // the first copies are on their way while the block sets up the rest
+    if (lane < 2 * ST + 1) mbar_init(&bars[lane], 1);
+    fence_barrier_init();
     __syncwarp();
-  } else if (warp == 5) {
-    tmem_alloc(tmem_slot, kTmemCols);
-    tmem_relinquish();
+    named_bar_arrive(1, kTileThreads);
+  } else {
+    if (warp == 5) {
+      tmem_alloc(tmem_slot, kTmemCols);
+      tmem_relinquish();
+    }
+    tc_fence_before();
+    named_bar_sync(1, kTileThreads);
+    tc_fence_after();
   }
-  tc_fence_before();
-  __syncthreads();
-  tc_fence_after();
-  const uint32_t tmem = *tmem_slot;
 
   if (warp == 4) {
     if (lane == 0) {
+      while (issued < ST && ks0 + issued < ks1) load(issued);
       while (ks0 + issued < ks1) {
         const int st = issued % ST;
         if (!mbar_wait(&empty[st], (uint32_t)((issued / ST - 1) & 1))) break;
@@ -244,6 +255,7 @@ linear_tile_kernel(const __grid_constant__ CUtensorMap tm_a,
     __syncwarp();
   } else if (warp == 5) {
     constexpr uint32_t idesc = idesc_f32acc(1, A_MN, B_MN, 128, BN);
+    tmem = *tmem_slot;
     uint32_t st = 0, phase = 0;
     for (int ks = ks0; ks < ks1; ++ks) {
       if (!mbar_wait_warp(&full[st], phase)) break;
@@ -262,112 +274,98 @@ linear_tile_kernel(const __grid_constant__ CUtensorMap tm_a,
     if (elect_one()) mma_commit(acc);
     __syncwarp();
   }
-  mbar_wait_warp(acc, 0);  // the sums are complete
+  mbar_wait_warp(acc, 0);  // the sums are complete (and tmem_slot long written)
   tc_fence_after();
+  tmem = *tmem_slot;
 
   const int m = 32 * (warp & 3) + lane;  // index along the 128 side
   const uint32_t lanes = (uint32_t)(32 * (warp & 3)) << 16;
   constexpr int kCols = BN >= 64 ? BN / 2 : BN;  // accumulator columns of a warp
   const int c0 = BN >= 64 ? kCols * (warp >> 2) : 0;
   const bool drains = BN >= 64 || warp < 4;
-  if (!SWAP && p.split == 1) {
-    cluster_wait();
+  cluster_wait();
+  const uint32_t log_s = 31u - (uint32_t)__clz(p.split);
+  const uint32_t dst = smem_u32(recv);
+  if (drains) {
 #pragma unroll
     for (int c = 0; c < kCols; c += 32) {
       uint32_t a[32];
       tmem_ld32(tmem + lanes + (uint32_t)(c0 + c), a);
       tmem_wait_ld();
-      if ((long long)a0 + m < p.rows) {
+      if (SWAP) {
+        // share of rank q: rows [q BN / S, ..) of BN; from rank r: [r][row][128]
+        const uint32_t per = BN >> log_s;
 #pragma unroll
-        for (int i = 0; i < 32; i += 8) {
-          if ((long long)b0 + c0 + c + i >= p.cols) continue;
-          float v[8];
-#pragma unroll
-          for (int j = 0; j < 8; ++j) v[j] = __uint_as_float(a[i + j]);
-          finish8(v, p.epi, (long long)a0 + m, (long long)b0 + c0 + c + i);
+        for (int i = 0; i < 32; ++i) {
+          const uint32_t r = (uint32_t)(c0 + c + i);
+          if (r >= BN || (long long)b0 + r >= p.rows) continue;
+          const uint32_t at = dst + ((rank * per + r % per) * 128 + (uint32_t)m) * 4;
+          if (p.split == 1)
+            st_shared_f1(at, a[i]);
+          else
+            st_cluster_f1(mapa(at, r / per), a[i]);
         }
-      }
-    }
-    tc_fence_before();
-  } else {
-    cluster_wait();
-    const uint32_t log_s = 31u - (uint32_t)__clz(p.split);
-    const uint32_t dst = smem_u32(recv);
-    if (drains) {
+      } else {
+        // share of rank q: columns [q BN / S, ..); from rank r: [r][128 rows][BN / S],
+        // 16-byte units of a row swizzled
+        const uint32_t per = (uint32_t)BN >> log_s, units = per / 4;
+        const uint32_t x = recv_swizzle((uint32_t)m, units);
+        if ((long long)a0 + m < p.rows) {
 #pragma unroll
-      for (int c = 0; c < kCols; c += 32) {
-        uint32_t a[32];
-        tmem_ld32(tmem + lanes + (uint32_t)(c0 + c), a);
-        tmem_wait_ld();
-        if (SWAP) {
-          // share of rank q: rows [q BN / S, ..) of BN; from rank r: [r][row][128]
-          const uint32_t per = BN >> log_s;
-#pragma unroll
-          for (int i = 0; i < 32; ++i) {
-            const uint32_t r = (uint32_t)(c0 + c + i);
-            if (r < BN && (long long)b0 + r < p.rows)
-              st_cluster_f1(mapa(dst + ((rank * per + r % per) * 128 + (uint32_t)m) * 4, r / per),
-                            a[i]);
-          }
-        } else {
-          // share of rank q: columns [q BN / S, ..); from rank r: [r][128 rows][BN / S],
-          // 16-byte units of a row swizzled
-          const uint32_t per = (uint32_t)BN >> log_s, units = per / 4;
-          const uint32_t x = recv_swizzle((uint32_t)m, units);
-          if ((long long)a0 + m < p.rows) {
-#pragma unroll
-            for (int i = 0; i < 32; i += 4) {
-              const uint32_t col = (uint32_t)(c0 + c + i), u = (col % per) / 4;
-              st_cluster_f4(mapa(dst + ((rank * 128 + (uint32_t)m) * units + (u ^ x)) * 16, col / per),
-                            a + i);
-            }
+          for (int i = 0; i < 32; i += 4) {
+            const uint32_t col = (uint32_t)(c0 + c + i), u = (col % per) / 4;
+            const uint32_t at = dst + ((rank * 128 + (uint32_t)m) * units + (u ^ x)) * 16;
+            if (p.split == 1)
+              st_shared_v4(at, a[i], a[i + 1], a[i + 2], a[i + 3]);
+            else
+              st_cluster_f4(mapa(at, col / per), a + i);
           }
         }
       }
     }
-    tc_fence_before();
-    __syncwarp();
-    cluster_arrive();
-    cluster_wait();
-    auto finish = [&](auto split) {
-      constexpr uint32_t S = decltype(split)::value;
-      constexpr uint32_t per = BN / S;
-      const float4* src = reinterpret_cast<const float4*>(recv);
-      constexpr uint32_t total = 128 * per / 8;  // pieces of 8 columns
+  }
+  tc_fence_before();
+  __syncwarp();
+  cluster_arrive();
+  cluster_wait();
+  auto finish = [&](auto split) {
+    constexpr uint32_t S = decltype(split)::value;
+    constexpr uint32_t per = BN / S;
+    const float4* src = reinterpret_cast<const float4*>(recv);
+    constexpr uint32_t total = 128 * per / 8;  // pieces of 8 columns
 #pragma unroll 2
-      for (uint32_t u = threadIdx.x; u < total; u += kTileThreads) {
-        const uint32_t row = SWAP ? u / 16 : u / (per / 8), c8 = SWAP ? u % 16 : u % (per / 8);
-        const long long orow = SWAP ? (long long)b0 + rank * per + row : (long long)a0 + row;
-        const long long ocol = SWAP ? (long long)a0 + 8 * c8 : (long long)b0 + rank * per + 8 * c8;
-        if (orow >= p.rows || ocol >= p.cols) continue;
-        float4 x[S], y[S];
+    for (uint32_t u = threadIdx.x; u < total; u += kTileThreads) {
+      const uint32_t row = SWAP ? u / 16 : u / (per / 8), c8 = SWAP ? u % 16 : u % (per / 8);
+      const long long orow = SWAP ? (long long)b0 + rank * per + row : (long long)a0 + row;
+      const long long ocol = SWAP ? (long long)a0 + 8 * c8 : (long long)b0 + rank * per + 8 * c8;
+      if (orow >= p.rows || ocol >= p.cols) continue;
+      float4 x[S], y[S];
 #pragma unroll
-        for (uint32_t q = 0; q < S; ++q) {
-          if (SWAP) {
-            x[q] = src[(q * per + row) * 32 + 2 * c8];
-            y[q] = src[(q * per + row) * 32 + 2 * c8 + 1];
-          } else {
-            constexpr uint32_t units = per / 4;
-            const uint32_t z = recv_swizzle(row, units);
-            x[q] = src[(q * 128 + row) * units + ((2 * c8) ^ z)];
-            y[q] = src[(q * 128 + row) * units + ((2 * c8 + 1) ^ z)];
-          }
+      for (uint32_t q = 0; q < S; ++q) {
+        if (SWAP) {
+          x[q] = src[(q * per + row) * 32 + 2 * c8];
+          y[q] = src[(q * per + row) * 32 + 2 * c8 + 1];
+        } else {
+          constexpr uint32_t units = per / 4;
+          const uint32_t z = recv_swizzle(row, units);
+          x[q] = src[(q * 128 + row) * units + ((2 * c8) ^ z)];
+          y[q] = src[(q * 128 + row) * units + ((2 * c8 + 1) ^ z)];
         }
-        float v[8] = {x[0].x, x[0].y, x[0].z, x[0].w, y[0].x, y[0].y, y[0].z, y[0].w};
-#pragma unroll
-        for (uint32_t q = 1; q < S; ++q) {
-          v[0] += x[q].x; v[1] += x[q].y; v[2] += x[q].z; v[3] += x[q].w;
-          v[4] += y[q].x; v[5] += y[q].y; v[6] += y[q].z; v[7] += y[q].w;
-        }
-        finish8(v, p.epi, orow, ocol);
       }
-    };
-    switch (p.split) {
-      case 1: finish(std::integral_constant<uint32_t, 1>{}); break;
-      case 2: finish(std::integral_constant<uint32_t, 2>{}); break;
-      case 4: finish(std::integral_constant<uint32_t, 4>{}); break;
-      default: finish(std::integral_constant<uint32_t, 8>{}); break;
+      float v[8] = {x[0].x, x[0].y, x[0].z, x[0].w, y[0].x, y[0].y, y[0].z, y[0].w};
+#pragma unroll
+      for (uint32_t q = 1; q < S; ++q) {
+        v[0] += x[q].x; v[1] += x[q].y; v[2] += x[q].z; v[3] += x[q].w;
+        v[4] += y[q].x; v[5] += y[q].y; v[6] += y[q].z; v[7] += y[q].w;
+      }
+      finish8(v, p.epi, orow, ocol);
     }
+  };
+  switch (p.split) {
+    case 1: finish(std::integral_constant<uint32_t, 1>{}); break;
+    case 2: finish(std::integral_constant<uint32_t, 2>{}); break;
+    case 4: finish(std::integral_constant<uint32_t, 4>{}); break;
+    default: finish(std::integral_constant<uint32_t, 8>{}); break;
   }
   __syncthreads();
   if (warp == 5) {
@@ -476,10 +474,12 @@ linear_pair_kernel(const __grid_constant__ CUtensorMap tm_a,
   const uint32_t rank = cluster_ctarank();
   const unsigned pair = blockIdx.x >> 1, npairs = gridDim.x >> 1;
   const bool has_res = p.epi.res != nullptr, has_pre = p.epi.pre != nullptr;
-  if (threadIdx.x == 0) {
-    for (int x = 0; x < Q_COUNT; ++x)
-      mbar_init(&bars[x], (x == Q_AEMPTY || x == Q_AEMPTY + 1) ? 2u * kEpiWarps : 1u);
+  if (threadIdx.x < Q_COUNT) {
+    const int x = (int)threadIdx.x;
+    mbar_init(&bars[x], (x == Q_AEMPTY || x == Q_AEMPTY + 1) ? 2u * kEpiWarps : 1u);
     fence_barrier_init();
+  }
+  if (warp == kEpiWarps && lane == 0) {
     tma_prefetch_desc(&tm_a);
     tma_prefetch_desc(&tm_b);
     tma_prefetch_desc(&io.out);
@@ -1048,7 +1048,7 @@ cudaError_t linear_gemm_launch(const GemmArgs& g, void* scratch, int sms, cudaSt
 namespace {
 
 constexpr int kActThreads = 256;
-constexpr int kBatch = 4;
+constexpr int kBatch = 3;
 constexpr int kActBlocks = 3;      // resident per SM
 constexpr int kActNarrowRows = 1024;
 
