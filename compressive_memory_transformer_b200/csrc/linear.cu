@@ -501,24 +501,26 @@ linear_pair_kernel(const __grid_constant__ CUtensorMap tm_a,
   bool ok = true;
 
   if (warp == kEpiWarps) {
-    if (lane == 0) {
-      int it = 0;
-      int issued[kPairStages] = {};
-      for (unsigned u = pair; ok && u < p.units; u += npairs) {
-        const unsigned t = u % p.tiles, part = u / p.tiles;
-        const int row = 256 * (int)(t / p.tiles_n) + 128 * (int)rank;
-        const int col = 256 * (int)(t % p.tiles_n) + 128 * (int)rank;
-        const int ks1 = (int)((long long)p.ksteps * (part + 1) / p.split);
-        for (int ks = (int)((long long)p.ksteps * part / p.split); ks < ks1; ++ks, ++it) {
-          const int st = it % kPairStages, use = it / kPairStages;
-          if (use > 0 && !mbar_wait(&bars[Q_EMPTY + st], (uint32_t)((use - 1) & 1))) {
-            ok = false;
-            break;
-          }
+    // The whole warp runs the loop and one elected lane issues: the values stay uniform, and
+    // the way to the copies short enough for a k-step's 512 cycles.
+    const uint32_t full0 = smem_cluster_addr(&bars[Q_FULL], 0);
+    int it = 0;
+    uint32_t st = 0, phase = 1;  // the first use of every stage waits for nothing
+    for (unsigned u = pair; ok && u < p.units; u += npairs) {
+      const unsigned t = u % p.tiles, part = u / p.tiles;
+      const int row = 256 * (int)(t / p.tiles_n) + 128 * (int)rank;
+      const int col = 256 * (int)(t % p.tiles_n) + 128 * (int)rank;
+      const int ks1 = (int)((long long)p.ksteps * (part + 1) / p.split);
+      for (int ks = (int)((long long)p.ksteps * part / p.split); ks < ks1; ++ks, ++it) {
+        if (!mbar_wait_warp(&bars[Q_EMPTY + st], phase)) {
+          ok = false;
+          break;
+        }
+        if (elect_one()) {
           uint8_t* sa = smem + st * kPairStage;
           uint8_t* sb = sa + kPairA;
           if (rank == 0) mbar_arrive_expect_tx(&bars[Q_FULL + st], 2 * kPairStage);
-          const uint32_t full = smem_cluster_addr(&bars[Q_FULL + st], 0);
+          const uint32_t full = full0 + 8 * st;
           const int k = kKStep * ks;
           if (A_MN) {
             tma_load_half(sa, &tm_a, full, row, k);
@@ -532,13 +534,14 @@ linear_pair_kernel(const __grid_constant__ CUtensorMap tm_a,
           } else {
             tma_load_half(sb, &tm_b, full, k, col);
           }
-          ++issued[st];
         }
+        __syncwarp();
+        if (++st == kPairStages) st = 0, phase ^= 1;
       }
-      // every copy into this CTA's ring has landed once its stage has been released
-      for (int st = 0; st < kPairStages; ++st)
-        if (issued[st] > 0) drain_wait(&bars[Q_EMPTY + st], (uint32_t)((issued[st] - 1) & 1));
     }
+    // every copy into this CTA's ring has landed once its stage has been released
+    if (lane < kPairStages && lane < it)
+      drain_wait(&bars[Q_EMPTY + lane], (uint32_t)(((it - 1 - lane) / kPairStages) & 1));
     __syncwarp();
   } else if (warp == kEpiWarps + 1) {
     if (rank == 0) {
