@@ -389,12 +389,16 @@ struct PairMaps {
   CUtensorMap out, res, pre;  // boxes of 32 columns x 32 rows, 64-byte swizzle
 };
 
-constexpr int kEpiWarps = 8;  // of a CTA: four lane quarters x two column halves
+// Epilogue warps of a CTA: four lane quarters x four parts of the columns. Half as many had
+// longer latencies to hide each: 131072 x 1024 x 4096 with tanh gelu 998 us against 932 (at
+// the power limit; without an activation 890 and 893).
+constexpr int kEpiWarps = 16;
+constexpr int kEpiCols = 1024 / kEpiWarps;  // columns of a warp
 constexpr int kPairThreads = 32 * (kEpiWarps + 2);
 constexpr int kPairStages = 5;
 constexpr int kPairA = 16384, kPairStage = 2 * kPairA;  // this CTA's half of A and of B
 constexpr int kSlot = 2048;                             // 32 rows x 64 bytes
-constexpr int kSlots = 4;                               // of an epilogue warp
+constexpr int kSlots = 2;                               // of an epilogue warp
 constexpr int kPairStaging = kEpiWarps * kSlots * kSlot;
 enum {
   Q_FULL = 0,
@@ -456,9 +460,8 @@ __device__ __forceinline__ uint32_t sw64(uint32_t r, uint32_t u) {
 // each CTA, both CTAs' copies completing on the even CTA's barrier. The epilogue takes 32
 // columns at a time: accumulator -> registers -> swizzled staging slot -> TMA store, which
 // writes whole sectors and clips at the edges; a residual comes into the same slot by a TMA
-// load ahead of time and is replaced by the output in place. A warp has four slots, so that
-// stores and loads are in flight while it works on the next columns: the chunks take them
-// in turn, or, with a pre-activation to write, two of them, the pre-activation the others.
+// load ahead of time and is replaced by the output in place. A warp has two slots: the chunks
+// take them in turn, or, with a pre-activation to write, the output one and it the other.
 template <bool A_MN, bool B_MN>
 __global__ void __launch_bounds__(kPairThreads, 1)
 linear_pair_kernel(const __grid_constant__ CUtensorMap tm_a,
@@ -598,33 +601,32 @@ linear_pair_kernel(const __grid_constant__ CUtensorMap tm_a,
     const bool res = has_res && p.split == 1;
     // chunk k of this warp (counted over its tiles) has slot k & mask, for the
     // (k >> turns)-th time; a residual is loaded `ahead` chunks before its use
-    const int turns = has_pre ? 1 : 2, mask = (1 << turns) - 1, ahead = turns;
+    const int turns = has_pre ? 0 : 1, mask = turns, ahead = turns;
     int lt = 0, chunk = 0, loads = 0;
     for (unsigned u = pair; ok && u < p.units; u += npairs, ++lt) {
       const unsigned t = u % p.tiles, part = u / p.tiles;
       const int acc = lt & 1;
       const long long row0 = 256ll * (t / p.tiles_n) + 128 * (int)rank + 32 * (warp & 3);
-      const long long col0 = 256ll * (t % p.tiles_n) + 128 * (warp >> 2);
+      const long long col0 = 256ll * (t % p.tiles_n) + kEpiCols * (warp >> 2);
       int n = 0;  // chunks of 32 columns that are inside
       if (row0 < p.rows && col0 < p.cols) {
         const long long left = (p.cols - col0 + 31) / 32;
-        n = left < 4 ? (int)left : 4;
+        n = left < kEpiCols / 32 ? (int)left : kEpiCols / 32;
       }
       auto load_res = [&](int c, int k) {  // chunk c of this tile, the k-th of this warp
         uint64_t* bar = &rbar[k & mask];
         mbar_arrive_expect_tx(bar, kSlot);
         tma_load_tile(slots + (k & mask) * kSlot, &io.res, bar, (int)col0 + 32 * c, (int)row0);
       };
-      if (res && n > 0) {
+      if (res && ahead && n > 0) {
         if (lane == 0) {
-          bulk_wait_read_but<1>();  // frees the slots of the next one or two chunks
+          bulk_wait_read_but<1>();  // frees the next chunk's slot
           load_res(0, chunk);
-          if (ahead == 2 && n > 1) load_res(1, chunk + 1);
         }
-        loads = chunk + (ahead < n ? ahead : n);
+        loads = chunk + 1;
       }
       // this tile's bias into L1 while its products run
-      if (p.epi.bias && p.split == 1 && lane < 4 && col0 + 32 * lane < p.cols)
+      if (p.epi.bias && p.split == 1 && lane < kEpiCols / 32 && col0 + 32 * lane < p.cols)
         asm volatile("prefetch.global.L1 [%0];" ::"l"(p.epi.bias + col0 + 32 * lane));
       if (!mbar_wait_warp(&bars[Q_AFULL + acc], (uint32_t)((lt >> 1) & 1))) {
         ok = false;
@@ -635,7 +637,7 @@ linear_pair_kernel(const __grid_constant__ CUtensorMap tm_a,
       for (int c = 0; c < n; ++c, ++chunk) {
         uint32_t a[32];
         float v[32];
-        tmem_ld32(tmem + (uint32_t)acc * 256 + lanes + (uint32_t)(128 * (warp >> 2) + 32 * c), a);
+        tmem_ld32(tmem + (uint32_t)acc * 256 + lanes + (uint32_t)(kEpiCols * (warp >> 2) + 32 * c), a);
         const long long col = col0 + 32 * c;
         if (p.epi.bias && p.split == 1) {
 #pragma unroll
@@ -651,17 +653,10 @@ linear_pair_kernel(const __grid_constant__ CUtensorMap tm_a,
         if (lane == 0) {
           // a residual further on, into a slot whose last store has been read; and the
           // slots written now (their stores are further back)
-          if (turns == 2) {
-            if (res)
-              bulk_wait_read_but<1>();
-            else
-              bulk_wait_read_but<3>();
-          } else {
-            if (res)
-              bulk_wait_read_but<0>();
-            else
-              bulk_wait_read_but<1>();
-          }
+          if (res)
+            bulk_wait_read_but<0>();
+          else
+            bulk_wait_read_but<1>();
           if (res && c + ahead < n) load_res(c + ahead, chunk + ahead);
         }
         if (res && c + ahead < n) loads = chunk + ahead + 1;
@@ -684,18 +679,28 @@ linear_pair_kernel(const __grid_constant__ CUtensorMap tm_a,
         for (int i = 0; i < 32; ++i) v[i] += __uint_as_float(a[i]);
         __syncwarp();
         const uint32_t so = smem_u32(slots + (chunk & mask) * kSlot);
-        if (has_pre) {
+        if (has_pre) {  // on its way before the activation
 #pragma unroll
           for (int q = 0; q < 4; ++q)
-            st_shared_v4(so + 2 * kSlot + sw64(lane, q), pack_bf16x2(v[8 * q], v[8 * q + 1]),
+            st_shared_v4(so + kSlot + sw64(lane, q), pack_bf16x2(v[8 * q], v[8 * q + 1]),
                          pack_bf16x2(v[8 * q + 2], v[8 * q + 3]),
                          pack_bf16x2(v[8 * q + 4], v[8 * q + 5]),
                          pack_bf16x2(v[8 * q + 6], v[8 * q + 7]));
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) {
+            tma_store_box(&io.pre, slots + kSlot, (int)col, (int)row0);
+            tma_store_commit();
+          }
         }
         with_act(p.epi.act, [&](auto k) {
 #pragma unroll
           for (int i = 0; i < 32; i += 2) act_pair<decltype(k)::value>(v[i], v[i + 1]);
         });
+        if (has_pre && !res) {  // the last output has been read from its slot
+          if (lane == 0) bulk_wait_read_but<1>();
+          __syncwarp();
+        }
         if (res) {
           if (!mbar_wait_warp(&rbar[chunk & mask], (uint32_t)((chunk >> turns) & 1))) {
             ok = false;
@@ -722,8 +727,6 @@ linear_pair_kernel(const __grid_constant__ CUtensorMap tm_a,
         __syncwarp();
         if (lane == 0) {
           tma_store_box(&io.out, slots + (chunk & mask) * kSlot, (int)col, (int)row0);
-          if (has_pre)
-            tma_store_box(&io.pre, slots + (2 + (chunk & mask)) * kSlot, (int)col, (int)row0);
           tma_store_commit();
         }
       }
