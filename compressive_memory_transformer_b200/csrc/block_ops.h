@@ -77,7 +77,7 @@ struct NormArgs {
 
 constexpr int kMaxNormDim = 8192;
 cudaError_t norm_set_attributes();
-bool norm_vectorised(const NormArgs& a, bool f32);
+int norm_piece(const NormArgs& a, bool f32);  // elements of a row per load
 cudaError_t norm_forward_launch(const NormArgs& a, int kind, bool f32, int sms,
                                 cudaStream_t stream);
 // Thread blocks of the backward, and chunks per gate group, for these sizes.

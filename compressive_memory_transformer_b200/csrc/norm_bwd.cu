@@ -51,10 +51,10 @@ __device__ __forceinline__ void centre(Row<kE>& t, const Row<kE>& vn, float inv_
   }
 }
 
-template <typename T, int TPR, bool VEC, bool LAYER>
+template <typename T, int TPR, int PIECE, bool LAYER>
 __global__ void __launch_bounds__(norm_threads(TPR), kResident / norm_threads(TPR))
 norm_backward_kernel(const NormArgs a) {
-  using L = RowLayout<T, TPR, VEC, kE>;
+  using L = RowLayout<T, TPR, PIECE, kE>;
   constexpr int kThreads = norm_threads(TPR), kWorkers = kThreads / TPR;
   constexpr int kSets = norm_sets(LAYER ? kNormLayer : kNormRms);
   __shared__ float2 sbuf[kWorkers][2][TPR / 32];
@@ -99,12 +99,12 @@ norm_backward_kernel(const NormArgs a) {
     Row<kE> pn, pd;  // sums over the unit's rows of d bn and of d
     INFINI_EACH_PAIR pn.p[i] = pd.p[i] = 0;
     for (long long row = r0; row < r1; ++row) {
-      RowRaw<T, TPR, VEC, kE> rx, rb, rr, rh;
+      RowRaw<T, TPR, PIECE, kE> rx, rb, rr, rh;
       rx.load(a.x, row, D, t);
       if (a.b) rb.load(a.b, row, D, t);
       // dh, and dr later, when registers are free again (fp32: both later)
       if (sizeof(T) == 2 && a.dh) rh.load(a.dh, row, D, t);
-      if (VEC && t == 0 && row + 1 < r1) {
+      if (PIECE * sizeof(T) == 16 && t == 0 && row + 1 < r1) {
         prefetch_row<T>(a.x, row + 1, D);
         if (a.b) prefetch_row<T>(a.b, row + 1, D);
         if (a.dh) prefetch_row<T>(a.dh, row + 1, D);
@@ -143,7 +143,7 @@ norm_backward_kernel(const NormArgs a) {
       }
       if (a.dx) {
         INFINI_EACH_PAIR v.p[i] = mul2(d.p[i], both(a.alpha));
-        store_row<T, TPR, VEC>(a.dx, row, D, t, v);
+        store_row<T, TPR, PIECE>(a.dx, row, D, t, v);
       }
       if (!a.b) continue;
       INFINI_EACH_PAIR {
@@ -155,7 +155,7 @@ norm_backward_kernel(const NormArgs a) {
         centre<LAYER>(d, bn, inv_d, red);
         INFINI_EACH_PAIR d.p[i] = mul2(d.p[i], both(inv_b));
       }
-      if (a.db) store_row<T, TPR, VEC>(a.db, row, D, t, d);
+      if (a.db) store_row<T, TPR, PIECE>(a.db, row, D, t, d);
     }
     // the unit's rows share a gate row
     if (a.post_w) {
@@ -217,23 +217,23 @@ cudaError_t with_tpr(int D, F&& f) {
   }
 }
 
-template <typename T, bool VEC, bool LAYER>
+template <typename T, int PIECE, bool LAYER>
 cudaError_t launch(const NormArgs& a, int blocks, cudaStream_t stream) {
   return with_tpr(a.D, [&](auto tpr) {
     constexpr int TPR = decltype(tpr)::value, kThreads = norm_threads(TPR);
-    norm_backward_kernel<T, TPR, VEC, LAYER>
+    norm_backward_kernel<T, TPR, PIECE, LAYER>
         <<<blocks, kThreads, slots_bytes(LAYER, kThreads), stream>>>(a);
     return cudaGetLastError();
   });
 }
 
-template <typename T, bool VEC, bool LAYER>
+template <typename T, int PIECE, bool LAYER>
 cudaError_t allow() {
   cudaError_t e = cudaSuccess;
   for (int d : {512, 1024, 2048, 4096, 8192}) {  // one width of each number of threads
     const cudaError_t f = with_tpr(d, [](auto tpr) {
       constexpr int TPR = decltype(tpr)::value;
-      return cudaFuncSetAttribute(norm_backward_kernel<T, TPR, VEC, LAYER>,
+      return cudaFuncSetAttribute(norm_backward_kernel<T, TPR, PIECE, LAYER>,
                                   cudaFuncAttributeMaxDynamicSharedMemorySize,
                                   slots_bytes(LAYER, norm_threads(TPR)));
     });
@@ -258,30 +258,33 @@ void norm_backward_plan(long long rows, int D, long long groups, int sms, int* b
 }
 
 cudaError_t norm_set_attributes() {
-  cudaError_t e = allow<__nv_bfloat16, true, false>();
-  if (e == cudaSuccess) e = allow<__nv_bfloat16, true, true>();
-  if (e == cudaSuccess) e = allow<__nv_bfloat16, false, false>();
-  if (e == cudaSuccess) e = allow<__nv_bfloat16, false, true>();
-  if (e == cudaSuccess) e = allow<float, true, false>();
-  if (e == cudaSuccess) e = allow<float, true, true>();
-  if (e == cudaSuccess) e = allow<float, false, false>();
-  if (e == cudaSuccess) e = allow<float, false, true>();
+  cudaError_t e = cudaSuccess;
+  for (auto f : {allow<__nv_bfloat16, 8, false>, allow<__nv_bfloat16, 8, true>,
+                 allow<__nv_bfloat16, 2, false>, allow<__nv_bfloat16, 2, true>,
+                 allow<__nv_bfloat16, 1, false>, allow<__nv_bfloat16, 1, true>,
+                 allow<float, 4, false>, allow<float, 4, true>, allow<float, 2, false>,
+                 allow<float, 2, true>, allow<float, 1, false>, allow<float, 1, true>})
+    if (e == cudaSuccess) e = f();
   return e;
 }
 
+namespace {
+template <typename T, int MOST>
+cudaError_t by_piece(const NormArgs& a, int kind, int piece, int blocks, cudaStream_t stream) {
+  const bool layer = kind == kNormLayer;
+  if (piece == MOST)
+    return layer ? launch<T, MOST, true>(a, blocks, stream) : launch<T, MOST, false>(a, blocks, stream);
+  if (piece == 2)
+    return layer ? launch<T, 2, true>(a, blocks, stream) : launch<T, 2, false>(a, blocks, stream);
+  return layer ? launch<T, 1, true>(a, blocks, stream) : launch<T, 1, false>(a, blocks, stream);
+}
+}  // namespace
+
 cudaError_t norm_backward_launch(const NormArgs& a, int kind, bool f32, int blocks,
                                  cudaStream_t stream) {
-  const bool vec = norm_vectorised(a, f32);
-  if (kind == kNormLayer) {
-    if (f32) return vec ? launch<float, true, true>(a, blocks, stream)
-                        : launch<float, false, true>(a, blocks, stream);
-    return vec ? launch<__nv_bfloat16, true, true>(a, blocks, stream)
-               : launch<__nv_bfloat16, false, true>(a, blocks, stream);
-  }
-  if (f32) return vec ? launch<float, true, false>(a, blocks, stream)
-                      : launch<float, false, false>(a, blocks, stream);
-  return vec ? launch<__nv_bfloat16, true, false>(a, blocks, stream)
-             : launch<__nv_bfloat16, false, false>(a, blocks, stream);
+  const int piece = norm_piece(a, f32);
+  return f32 ? by_piece<float, 4>(a, kind, piece, blocks, stream)
+             : by_piece<__nv_bfloat16, 8>(a, kind, piece, blocks, stream);
 }
 
 }  // namespace infini

@@ -2,11 +2,11 @@
 // loads and stores, and sums over a row's threads.
 //
 // A row of D elements belongs to TPR threads of a block (a "worker"); each thread holds E
-// (16 or 32) elements as fp32 pairs, on which the arithmetic is packed (f32x2). Vector layout
-// (16-byte pieces): piece j of thread t is the (t + j TPR)-th of the row, so that
-// neighbouring threads read neighbouring pieces; 8 elements each of bf16, 4 of fp32. Scalar
-// layout, for odd widths and rows that do not start on 16 bytes: element t + i TPR for
-// i = 0..E - 1. Elements outside the row are held as 0.
+// (16 or 32) elements as fp32 pairs, on which the arithmetic is packed (f32x2). Elements come
+// in pieces of PIECE neighbours, one load each, 16 bytes where every row starts on 16 bytes
+// and is a whole number of them, fewer where widths or addresses are odd: piece j of thread t is
+// the (t + j TPR)-th of the row, so that neighbouring threads read neighbouring pieces.
+// Elements outside the row are held as 0.
 #pragma once
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
@@ -34,10 +34,10 @@ struct Row {
 };
 #define INFINI_EACH_PAIR _Pragma("unroll") for (int i = 0; i < kE / 2; ++i)
 
-template <typename T, int TPR, bool VEC, int E>
+template <typename T, int TPR, int PIECE, int E>
 struct RowLayout {
   static constexpr int kE = E;
-  static constexpr int kPiece = VEC ? 16 / (int)sizeof(T) : 1;  // elements of a piece
+  static constexpr int kPiece = PIECE;  // elements of a piece
   static constexpr int kPieces = kE / kPiece;
   // Column of element e of thread t.
   __device__ static __forceinline__ int col(int t, int e) {
@@ -46,25 +46,36 @@ struct RowLayout {
 };
 
 // One row's elements of one thread as loaded.
-template <typename T, int TPR, bool VEC, int kE>
+template <typename T, int TPR, int PIECE, int kE>
 struct RowRaw {
-  using L = RowLayout<T, TPR, VEC, kE>;
+  using L = RowLayout<T, TPR, PIECE, kE>;
   uint32_t w[kE * sizeof(T) / 4];
 
   __device__ __forceinline__ void load(const void* base, long long row, int D, int t) {
     const T* p = static_cast<const T*>(base) + row * D;
-    if constexpr (VEC) {
+    constexpr int kBytes = PIECE * (int)sizeof(T);
+    if constexpr (kBytes == 16) {
 #pragma unroll
       for (int j = 0; j < L::kPieces; ++j) {
         uint4 v = make_uint4(0, 0, 0, 0);
-        const int c = L::col(t, j * L::kPiece);
+        const int c = L::col(t, j * PIECE);
         if (c < D) v = __ldcs(reinterpret_cast<const uint4*>(p + c));
         w[4 * j] = v.x; w[4 * j + 1] = v.y; w[4 * j + 2] = v.z; w[4 * j + 3] = v.w;
       }
-    } else if constexpr (sizeof(T) == 4) {
+    } else if constexpr (kBytes == 8) {
 #pragma unroll
-      for (int i = 0; i < kE; ++i)
-        w[i] = L::col(t, i) < D ? reinterpret_cast<const uint32_t*>(p)[L::col(t, i)] : 0u;
+      for (int j = 0; j < L::kPieces; ++j) {
+        uint2 v = make_uint2(0, 0);
+        const int c = L::col(t, j * PIECE);
+        if (c < D) v = __ldcs(reinterpret_cast<const uint2*>(p + c));
+        w[2 * j] = v.x; w[2 * j + 1] = v.y;
+      }
+    } else if constexpr (kBytes == 4) {
+#pragma unroll
+      for (int j = 0; j < L::kPieces; ++j) {
+        const int c = L::col(t, j * PIECE);
+        w[j] = c < D ? __ldcs(reinterpret_cast<const unsigned*>(p + c)) : 0u;
+      }
     } else {
       const uint16_t* q = reinterpret_cast<const uint16_t*>(p);
 #pragma unroll
@@ -87,15 +98,16 @@ struct RowRaw {
   }
 };
 
-template <typename T, int TPR, bool VEC, int kE>
+template <typename T, int TPR, int PIECE, int kE>
 __device__ __forceinline__ void store_row(void* base, long long row, int D, int t,
                                           const Row<kE>& v) {
-  using L = RowLayout<T, TPR, VEC, kE>;
+  using L = RowLayout<T, TPR, PIECE, kE>;
   T* p = static_cast<T*>(base) + row * D;
-  if constexpr (VEC) {
+  constexpr int kBytes = PIECE * (int)sizeof(T);
+  if constexpr (kBytes == 16) {
 #pragma unroll
     for (int j = 0; j < L::kPieces; ++j) {
-      const int c = L::col(t, j * L::kPiece);
+      const int c = L::col(t, j * PIECE);
       if (c >= D) continue;
       uint4 o;
       if constexpr (sizeof(T) == 2)
@@ -108,16 +120,33 @@ __device__ __forceinline__ void store_row(void* base, long long row, int D, int 
                        (uint32_t)v.p[2 * j + 1], (uint32_t)(v.p[2 * j + 1] >> 32));
       *reinterpret_cast<uint4*>(p + c) = o;
     }
+  } else if constexpr (kBytes >= 4) {
+    constexpr int kWords = kBytes / 4;
+#pragma unroll
+    for (int j = 0; j < L::kPieces; ++j) {
+      const int c = L::col(t, j * PIECE);
+      if (c >= D) continue;
+      uint32_t o[kWords];
+#pragma unroll
+      for (int k = 0; k < kWords; ++k) {
+        if constexpr (sizeof(T) == 2) {
+          const uint64_t f = v.p[(PIECE * j) / 2 + k];
+          o[k] = pack_bf16x2(lo_of(f), hi_of(f));
+        } else {
+          const uint64_t f = v.p[(PIECE * j + k) / 2];
+          o[k] = (PIECE * j + k) % 2 ? (uint32_t)(f >> 32) : (uint32_t)f;
+        }
+      }
+      if constexpr (kBytes == 8)
+        *reinterpret_cast<uint2*>(p + c) = make_uint2(o[0], o[1]);
+      else
+        *reinterpret_cast<uint32_t*>(p + c) = o[0];
+    }
   } else {
 #pragma unroll
     for (int e = 0; e < kE; ++e)
-      if (L::col(t, e) < D) {
-        const float f = e % 2 ? hi_of(v.p[e / 2]) : lo_of(v.p[e / 2]);
-        if constexpr (sizeof(T) == 2)
-          p[L::col(t, e)] = __float2bfloat16(f);
-        else
-          p[L::col(t, e)] = f;
-      }
+      if (L::col(t, e) < D)
+        p[L::col(t, e)] = __float2bfloat16(e % 2 ? hi_of(v.p[e / 2]) : lo_of(v.p[e / 2]));
   }
 }
 
@@ -142,6 +171,13 @@ __device__ __forceinline__ Row<L::kE> load_param(const float* p, int D, int t) {
                      : "l"(p + c));
 #pragma unroll
       for (int i = 0; i < 4; ++i) r.p[e / 2 + i] = f2pack(f[2 * i], f[2 * i + 1]);
+    }
+  } else if constexpr (L::kPiece == 2) {
+    INFINI_EACH_PAIR {
+      const int c = L::col(t, 2 * i);
+      float2 f = make_float2(0.f, 0.f);
+      if (c < D) f = __ldg(reinterpret_cast<const float2*>(p + c));
+      r.p[i] = f2pack(f.x, f.y);
     }
   } else if constexpr (L::kPiece > 1) {
 #pragma unroll

@@ -11,7 +11,7 @@ pytestmark = pytest.mark.gpu
 BF, F32 = torch.bfloat16, torch.float32
 EPS = 1e-5
 # one element, fewer than a vector, each number of threads per row, odd widths, the largest
-DIMS = [1, 7, 8, 77, 128, 256, 264, 777, 1000, 1024, 1032, 2048, 2056, 4095, 4096, 5000, 8192]
+DIMS = [1, 2, 7, 8, 77, 78, 128, 256, 264, 777, 1000, 1024, 1032, 1030, 2048, 2056, 4094, 4095, 4096, 5000, 8192]
 
 
 @pytest.fixture(scope="module")
