@@ -27,10 +27,12 @@ namespace {
 constexpr int kResident = 512;  // threads per SM: 128 registers each
 constexpr int kE = 16;          // elements per thread
 
-// Shared memory of a block: its sums over rows, and gate times w (and c).
+// Shared memory of a block: its sums over rows, and gate times w (layer norms: and c, and the
+// unit's sum of d).
 constexpr int slots_bytes(bool layer, int threads) {
-  return (layer ? norm_sets(kNormLayer) + 2 : norm_sets(kNormRms) + 1) * (kE / 2) * threads * 8;
+  return (layer ? norm_sets(kNormLayer) + 3 : norm_sets(kNormRms) + 1) * (kE / 2) * threads * 8;
 }
+static_assert(slots_bytes(true, 512) <= 227 * 1024, "shared memory of a block");
 
 // The part of a norm's gradient that both norms share: with t the gradient of n(v) and vn =
 // n(v), t - [mean t] - vn mean(t vn), in place of t (to be multiplied by n's factor).
@@ -96,8 +98,11 @@ norm_backward_kernel(const NormArgs a) {
         if (shift) slot(kSets + 1, i) = k.p[i];
       }
     }
-    Row<kE> pn, pd;  // sums over the unit's rows of d bn and of d
-    INFINI_EACH_PAIR pn.p[i] = pd.p[i] = 0;
+    Row<kE> pn;  // sum over the unit's rows of d bn; of d: slot(kSets + 2)
+    INFINI_EACH_PAIR {
+      pn.p[i] = 0;
+      if constexpr (LAYER) slot(kSets + 2, i) = 0;
+    }
     for (long long row = r0; row < r1; ++row) {
       RowRaw<T, TPR, PIECE, kE> rx, rb, rr, rh;
       rx.load(a.x, row, D, t);
@@ -148,7 +153,7 @@ norm_backward_kernel(const NormArgs a) {
       if (!a.b) continue;
       INFINI_EACH_PAIR {
         pn.p[i] = fma2(d.p[i], bn.p[i], pn.p[i]);
-        if constexpr (LAYER) pd.p[i] = add2(pd.p[i], d.p[i]);
+        if constexpr (LAYER) slot(kSets + 2, i) = add2(slot(kSets + 2, i), d.p[i]);
         d.p[i] = mul2(d.p[i], slot(kSets, i));
       }
       if (a.post_w) {
@@ -159,7 +164,8 @@ norm_backward_kernel(const NormArgs a) {
     }
     // the unit's rows share a gate row
     if (a.post_w) {
-      Row<kE> e = pn, f = pd;
+      Row<kE> e = pn, f;
+      if constexpr (LAYER) INFINI_EACH_PAIR f.p[i] = slot(kSets + 2, i);
       if (a.gate) {
         const Row<kE> q = load_param<L>(a.gate + g * D, D, t);
         INFINI_EACH_PAIR {
@@ -178,7 +184,7 @@ norm_backward_kernel(const NormArgs a) {
         INFINI_EACH_PAIR pn.p[i] = mul2(pn.p[i], q.p[i]);
         if (LAYER && a.post_b) {
           const Row<kE> k = load_param<L>(a.post_b, D, t);
-          INFINI_EACH_PAIR pn.p[i] = fma2(pd.p[i], k.p[i], pn.p[i]);
+          INFINI_EACH_PAIR pn.p[i] = fma2(slot(kSets + 2, i), k.p[i], pn.p[i]);
         }
       }
       float* dst = a.gpart + u0 * D;
