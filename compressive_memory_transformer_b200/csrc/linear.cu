@@ -387,7 +387,7 @@ struct PairParams {
 };
 
 struct PairMaps {
-  CUtensorMap out, res, pre;  // boxes of 32 columns x 32 rows, 64-byte swizzle
+  CUtensorMap out, res, pre;  // boxes of 64 columns x 32 rows, 128-byte swizzle
 };
 
 // Epilogue warps of a CTA: four lane quarters x four parts of the columns. Half as many had
@@ -398,17 +398,17 @@ constexpr int kEpiCols = 1024 / kEpiWarps;  // columns of a warp
 constexpr int kPairThreads = 32 * (kEpiWarps + 2);
 constexpr int kPairStages = 5;
 constexpr int kPairA = 16384, kPairStage = 2 * kPairA;  // this CTA's half of A and of B
-constexpr int kSlot = 2048;                             // 32 rows x 64 bytes
-constexpr int kSlots = 2;                               // of an epilogue warp
-constexpr int kPairStaging = kEpiWarps * kSlots * kSlot;
+constexpr int kSlot = 32 * 128;                         // staging of a warp: 32 rows, 64 columns
+constexpr int kPairStaging = kEpiWarps * kSlot;
+static_assert(kEpiCols == 64, "one box of columns per warp");
 enum {
   Q_FULL = 0,
   Q_EMPTY = Q_FULL + kPairStages,
   Q_AFULL = Q_EMPTY + kPairStages,
   Q_AEMPTY = Q_AFULL + 2,
   Q_DRAIN = Q_AEMPTY + 2,
-  Q_RES = Q_DRAIN + 1,  // one per staging slot
-  Q_COUNT = Q_RES + kSlots * kEpiWarps
+  Q_RES = Q_DRAIN + 1,  // one per epilogue warp
+  Q_COUNT = Q_RES + kEpiWarps
 };
 constexpr int kPairBars = 512;
 static_assert(Q_COUNT * 8 + 4 <= kPairBars, "barrier area");
@@ -435,12 +435,6 @@ __device__ __forceinline__ void tma_store_box(const CUtensorMap* m, const void* 
       : "memory");
 }
 
-// Until at most N of this thread's bulk store groups still read shared memory.
-template <int N>
-__device__ __forceinline__ void bulk_wait_read_but() {
-  asm volatile("cp.async.bulk.wait_group.read %0;" ::"n"(N) : "memory");
-}
-
 __device__ __forceinline__ uint4 ld_shared_v4(uint32_t addr) {
   uint4 v;
   asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
@@ -450,22 +444,20 @@ __device__ __forceinline__ uint4 ld_shared_v4(uint32_t addr) {
   return v;
 }
 
-// Place of 16-byte unit u (0..3) of row r in a box with the 64-byte swizzle.
-__device__ __forceinline__ uint32_t sw64(uint32_t r, uint32_t u) {
-  return r * 64u + ((u ^ ((r >> 1) & 3u)) << 4);
-}
-
 // Warps 0-15 of each CTA: epilogue (warp w drains accumulator lanes 32 (w % 4).. and columns
 // 64 (w / 4)..); warp 16: copies; warp 17 of the even CTA: the pair's products (M = 256,
 // N = 256, K = 16 each). Each k-step of 64 brings 128 rows (columns) of A and of B into
-// each CTA, both CTAs' copies completing on the even CTA's barrier. The epilogue takes 32
-// columns at a time: accumulator -> registers -> swizzled staging slot -> TMA store, which
-// writes whole sectors and clips at the edges; a residual comes into the same slot by a TMA
-// load ahead of time and is replaced by the output in place. A warp has two slots: the chunks
-// take them in turn, or, with a pre-activation to write, the output one and it the other.
+// each CTA, both CTAs' copies completing on the even CTA's barrier. An epilogue warp's 32
+// rows x 64 columns go from the accumulator through registers into its swizzled staging slot
+// and out by one TMA store of whole 128-byte lines, clipped at the edges; a residual comes
+// into the slot by a TMA load while the products still run and is replaced by the output in
+// place; a pre-activation goes out through the slot first. The accumulator is read 32 columns
+// at a time (twice with a pre-activation).
 // Bound by the tensor cores, and over seconds by the power limit: 131072 x 1024 x 4096 in
-// 765 us (1440 TFLOP/s, 85% of the measured burst peak; cuBLAS 756), at the limit 885 (892),
-// with bias and tanh gelu 924, with the pre-activation stored too 1045.
+// 788 us (1395 TFLOP/s, 82% of the measured burst peak; cuBLAS 756), at the limit 912 (905),
+// with bias and tanh gelu 932, with the pre-activation stored too 1082. Two boxes of 32
+// columns per warp with a slot each were 1 to 2.5% faster there but 5 to 14% slower where a
+// launch has few tiles per pair (8192 x 1024 x 1024: 18.1 us, now 16.9; cuBLAS 15.0).
 template <bool A_MN, bool B_MN>
 __global__ void __launch_bounds__(kPairThreads, 1)
 linear_pair_kernel(const __grid_constant__ CUtensorMap tm_a,
@@ -600,119 +592,126 @@ linear_pair_kernel(const __grid_constant__ CUtensorMap tm_a,
     __syncwarp();
   } else {
     const uint32_t lanes = (uint32_t)(32 * (warp & 3)) << 16;
-    uint8_t* slots = staging + warp * kSlots * kSlot;
-    uint64_t* rbar = &bars[Q_RES + kSlots * warp];
-    const bool res = has_res && p.split == 1;
-    // chunk k of this warp (counted over its tiles) has slot k & mask, for the
-    // (k >> turns)-th time; a residual is loaded `ahead` chunks before its use
-    const int turns = has_pre ? 0 : 1, mask = turns, ahead = turns;
-    int lt = 0, chunk = 0, loads = 0;
+    uint8_t* slot = staging + warp * kSlot;
+    const uint32_t so = smem_u32(slot);
+    uint64_t* rbar = &bars[Q_RES + warp];
+    const bool res = has_res && p.split == 1, bias = p.epi.bias && p.split == 1;
+    int lt = 0, loads = 0;  // residual copies asked for; every one but the last waited for
+    auto pack32 = [&](int half, const float (&v)[32]) {
+#pragma unroll
+      for (int q = 0; q < 4; ++q)
+        st_shared_v4(so + sw128(lane, 4 * half + q), pack_bf16x2(v[8 * q], v[8 * q + 1]),
+                     pack_bf16x2(v[8 * q + 2], v[8 * q + 3]),
+                     pack_bf16x2(v[8 * q + 4], v[8 * q + 5]),
+                     pack_bf16x2(v[8 * q + 6], v[8 * q + 7]));
+    };
     for (unsigned u = pair; ok && u < p.units; u += npairs, ++lt) {
       const unsigned t = u % p.tiles, part = u / p.tiles;
       const int acc = lt & 1;
       const long long row0 = 256ll * (t / p.tiles_n) + 128 * (int)rank + 32 * (warp & 3);
       const long long col0 = 256ll * (t % p.tiles_n) + kEpiCols * (warp >> 2);
-      int n = 0;  // chunks of 32 columns that are inside
-      if (row0 < p.rows && col0 < p.cols) {
-        const long long left = (p.cols - col0 + 31) / 32;
-        n = left < kEpiCols / 32 ? (int)left : kEpiCols / 32;
-      }
-      auto load_res = [&](int c, int k) {  // chunk c of this tile, the k-th of this warp
-        uint64_t* bar = &rbar[k & mask];
-        mbar_arrive_expect_tx(bar, kSlot);
-        tma_load_tile(slots + (k & mask) * kSlot, &io.res, bar, (int)col0 + 32 * c, (int)row0);
+      const bool in = row0 < p.rows && col0 < p.cols;
+      const uint32_t ta = tmem + (uint32_t)acc * 256 + lanes + (uint32_t)(kEpiCols * (warp >> 2));
+      auto load_res = [&]() {
+        bulk_wait_group_read0();  // the slot's last store has been read
+        mbar_arrive_expect_tx(rbar, kSlot);
+        tma_load_tile(slot, &io.res, rbar, (int)col0, (int)row0);
       };
-      if (res && ahead && n > 0) {
-        if (lane == 0) {
-          bulk_wait_read_but<1>();  // frees the next chunk's slot
-          load_res(0, chunk);
-        }
-        loads = chunk + 1;
-      }
-      // this tile's bias into L1 while its products run
-      if (p.epi.bias && p.split == 1 && lane < kEpiCols / 32 && col0 + 32 * lane < p.cols)
-        asm volatile("prefetch.global.L1 [%0];" ::"l"(p.epi.bias + col0 + 32 * lane));
-      if (!mbar_wait_warp(&bars[Q_AFULL + acc], (uint32_t)((lt >> 1) & 1))) {
-        ok = false;
-        break;
-      }
-      tc_fence_after();
-#pragma unroll 1
-      for (int c = 0; c < n; ++c, ++chunk) {
+      // acc + bias of 32 columns
+      auto sums = [&](int half, float (&v)[32]) {
         uint32_t a[32];
-        float v[32];
-        tmem_ld32(tmem + (uint32_t)acc * 256 + lanes + (uint32_t)(kEpiCols * (warp >> 2) + 32 * c), a);
-        const long long col = col0 + 32 * c;
-        if (p.epi.bias && p.split == 1) {
+        tmem_ld32(ta + 32 * half, a);
+        if (bias) {
 #pragma unroll
           for (int i = 0; i < 32; i += 4) {
             float4 b = make_float4(0.f, 0.f, 0.f, 0.f);
-            if (col + i < p.cols) b = __ldg(reinterpret_cast<const float4*>(p.epi.bias + col + i));
+            const long long col = col0 + 32 * half + i;
+            if (col < p.cols) b = __ldg(reinterpret_cast<const float4*>(p.epi.bias + col));
             v[i] = b.x; v[i + 1] = b.y; v[i + 2] = b.z; v[i + 3] = b.w;
           }
         } else {
 #pragma unroll
           for (int i = 0; i < 32; ++i) v[i] = 0.f;
         }
-        if (lane == 0) {
-          // a residual further on, into a slot whose last store has been read; and the
-          // slots written now (their stores are further back)
-          if (res)
-            bulk_wait_read_but<0>();
-          else
-            bulk_wait_read_but<1>();
-          if (res && c + ahead < n) load_res(c + ahead, chunk + ahead);
-        }
-        if (res && c + ahead < n) loads = chunk + ahead + 1;
         tmem_wait_ld();
-        if (c == n - 1) {  // the accumulator may take the next tile
-          tc_fence_before();
-          __syncwarp();
-          if (lane == 0) mbar_arrive_cluster(smem_cluster_addr(&bars[Q_AEMPTY + acc], 0));
-        }
-        if (p.split > 1) {
-          if (row0 + lane < p.rows) {
-            float* dst = p.partial + ((long long)part * p.rows + row0 + lane) * p.cols + col;
-#pragma unroll
-            for (int i = 0; i < 32; i += 8)
-              if (col + i < p.cols) st_global_v8(dst + i, a + i);
-          }
-          continue;
-        }
 #pragma unroll
         for (int i = 0; i < 32; ++i) v[i] += __uint_as_float(a[i]);
+      };
+      auto release = [&]() {  // the accumulator may take the next tile
+        tc_fence_before();
         __syncwarp();
-        const uint32_t so = smem_u32(slots + (chunk & mask) * kSlot);
-        if (has_pre) {  // on its way before the activation
+        if (lane == 0) mbar_arrive_cluster(smem_cluster_addr(&bars[Q_AEMPTY + acc], 0));
+      };
+      if (res && !has_pre && in) {
+        if (lane == 0) load_res();
+        ++loads;
+      }
+      // this tile's bias into L1 while its products run
+      if (bias && lane < kEpiCols / 32 && col0 + 32 * lane < p.cols)
+        asm volatile("prefetch.global.L1 [%0];" ::"l"(p.epi.bias + col0 + 32 * lane));
+      if (!mbar_wait_warp(&bars[Q_AFULL + acc], (uint32_t)((lt >> 1) & 1))) {
+        ok = false;
+        break;
+      }
+      tc_fence_after();
+      if (!in) {
+        release();
+        continue;
+      }
+      float v[32];
+      if (p.split > 1) {
+#pragma unroll 1
+        for (int half = 0; half < 2; ++half) {
+          sums(half, v);
+          if (row0 + lane < p.rows) {
+            float* dst = p.partial + ((long long)part * p.rows + row0 + lane) * p.cols + col0;
 #pragma unroll
-          for (int q = 0; q < 4; ++q)
-            st_shared_v4(so + kSlot + sw64(lane, q), pack_bf16x2(v[8 * q], v[8 * q + 1]),
-                         pack_bf16x2(v[8 * q + 2], v[8 * q + 3]),
-                         pack_bf16x2(v[8 * q + 4], v[8 * q + 5]),
-                         pack_bf16x2(v[8 * q + 6], v[8 * q + 7]));
-          fence_proxy_async_smem();
-          __syncwarp();
-          if (lane == 0) {
-            tma_store_box(&io.pre, slots + kSlot, (int)col, (int)row0);
-            tma_store_commit();
+            for (int i = 0; i < 32; i += 8)
+              if (col0 + 32 * half + i < p.cols)
+                st_global_v8(dst + 32 * half + i, reinterpret_cast<const uint32_t*>(v + i));
           }
         }
+        release();
+        continue;
+      }
+      if (has_pre) {
+        if (lane == 0) bulk_wait_group_read0();
+        __syncwarp();
+#pragma unroll 1
+        for (int half = 0; half < 2; ++half) {
+          sums(half, v);
+          pack32(half, v);
+        }
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) {
+          tma_store_box(&io.pre, slot, (int)col0, (int)row0);
+          tma_store_commit();
+          if (res) load_res();
+        }
+        if (res) ++loads;
+      }
+      if (res) {
+        if (!mbar_wait_warp(rbar, (uint32_t)((loads - 1) & 1))) {
+          ok = false;
+          break;
+        }
+      } else {
+        if (lane == 0) bulk_wait_group_read0();
+        __syncwarp();
+      }
+#pragma unroll 1
+      for (int half = 0; half < 2; ++half) {
+        sums(half, v);
+        if (half == 1) release();
         with_act(p.epi.act, [&](auto k) {
 #pragma unroll
           for (int i = 0; i < 32; i += 2) act_pair<decltype(k)::value>(v[i], v[i + 1]);
         });
-        if (has_pre && !res) {  // the last output has been read from its slot
-          if (lane == 0) bulk_wait_read_but<1>();
-          __syncwarp();
-        }
         if (res) {
-          if (!mbar_wait_warp(&rbar[chunk & mask], (uint32_t)((chunk >> turns) & 1))) {
-            ok = false;
-            break;
-          }
 #pragma unroll
           for (int q = 0; q < 4; ++q) {
-            const uint4 r = ld_shared_v4(so + sw64(lane, q));
+            const uint4 r = ld_shared_v4(so + sw128(lane, 4 * half + q));
             const uint32_t w[4] = {r.x, r.y, r.z, r.w};
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
@@ -721,31 +720,19 @@ linear_pair_kernel(const __grid_constant__ CUtensorMap tm_a,
             }
           }
         }
-#pragma unroll
-        for (int q = 0; q < 4; ++q)
-          st_shared_v4(so + sw64(lane, q), pack_bf16x2(v[8 * q], v[8 * q + 1]),
-                       pack_bf16x2(v[8 * q + 2], v[8 * q + 3]),
-                       pack_bf16x2(v[8 * q + 4], v[8 * q + 5]),
-                       pack_bf16x2(v[8 * q + 6], v[8 * q + 7]));
-        fence_proxy_async_smem();
-        __syncwarp();
-        if (lane == 0) {
-          tma_store_box(&io.out, slots + (chunk & mask) * kSlot, (int)col, (int)row0);
-          tma_store_commit();
-        }
+        pack32(half, v);
       }
-      if (n == 0) {
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive_cluster(smem_cluster_addr(&bars[Q_AEMPTY + acc], 0));
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) {
+        tma_store_box(&io.out, slot, (int)col0, (int)row0);
+        tma_store_commit();
       }
     }
     if (lane == 0) {
-      // residual copies that a given-up wait left behind have landed, and every store has
+      // a residual copy that a given-up wait left behind has landed, and every store has
       // been read from shared memory
-      if (!ok)
-        for (int k = loads > mask + 1 ? loads - mask - 1 : 0; k < loads; ++k)
-          drain_wait(&rbar[k & mask], (uint32_t)((k >> turns) & 1));
+      if (!ok && loads > 0) drain_wait(rbar, (uint32_t)((loads - 1) & 1));
       bulk_wait_group_read0();
     }
     __syncwarp();
@@ -781,34 +768,33 @@ split_reduce_kernel(const float* __restrict__ partial, int split, long long rows
 
 // ---- host side --------------------------------------------------------------------------
 
-// Map over a stored matrix [outer][inner], rows ld elements apart; boxes of 64 (swizzle
-// 128 bytes) or 32 (64 bytes) inner x box_outer outer elements. Reads outside the matrix
-// give zeros, stores outside it are dropped.
+// Map over a stored matrix [outer][inner], rows ld elements apart; boxes of 64 inner x
+// box_outer outer elements, 128-byte swizzle. Reads outside the matrix give zeros, stores
+// outside it are dropped.
 bool make_map(CUtensorMap* m, const void* base, long long inner, long long outer, long long ld,
-              uint32_t box_inner, uint32_t box_outer) {
+              uint32_t box_outer) {
   EncodeTiledFn enc = get_encode_fn();
   if (!enc) return false;
   const cuuint64_t dims[2] = {(cuuint64_t)inner, (cuuint64_t)outer};
   const cuuint64_t strides[1] = {(cuuint64_t)ld * 2};
-  const cuuint32_t box[2] = {box_inner, box_outer};
+  const cuuint32_t box[2] = {64, box_outer};
   const cuuint32_t estr[2] = {1, 1};
   return enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(base), dims, strides, box,
-             estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
-             box_inner == 64 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
+             estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
              CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 // Map of an operand whose tile is `mn` rows or columns wide.
 bool operand_map(CUtensorMap* m, const __nv_bfloat16* p, long long ld, bool mn_major,
                  long long extent, long long R, int mn) {
-  return mn_major ? make_map(m, p, extent, R, ld, 64, 64)
-                  : make_map(m, p, R, extent, ld, 64, (uint32_t)mn);
+  return mn_major ? make_map(m, p, extent, R, ld, 64)
+                  : make_map(m, p, R, extent, ld, (uint32_t)mn);
 }
 
-// Map of an output (or residual) in boxes of 32 columns x 32 rows, 64-byte swizzle.
+// Map of an output (or residual) in boxes of 64 columns x 32 rows, 128-byte swizzle.
 bool box_map(CUtensorMap* m, const __nv_bfloat16* p, long long rows, long long cols,
              long long ld) {
-  return make_map(m, p, cols, rows, ld, 32, 32);
+  return make_map(m, p, cols, rows, ld, 32);
 }
 
 // CTA pairs that can be resident at once, looked up once per device.
@@ -984,7 +970,7 @@ double pair_time(long long P, long long Q, int split, long long units, long long
                  int sms) {
   const long long pairs = sms / 2, part = (ksteps + split - 1) / split;
   const double waves = (double)((units + pairs - 1) / pairs);
-  double t = 7.2 + waves * (part * 0.31 > 2.5 ? part * 0.31 : 2.5);
+  double t = 6.6 + waves * (part * 0.31 > 1.9 ? part * 0.31 : 1.9);
   if (split > 1) t += 3.0 + (double)split * P * Q * 8 / 8e6;
   return t;
 }

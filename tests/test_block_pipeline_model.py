@@ -12,18 +12,17 @@ from test_pipeline_model import Sim
 WARPS = 16
 
 
-def pair_roles(sim, units, stages=5, res=False, pre=False, chunks=2):
+def pair_roles(sim, units, stages=5, res=False, pre=False):
     """units: k-steps of each unit of this pair, in order. One epilogue warp per CTA stands
-    for the sixteen (each arrives for its own share); its residual copies are modelled one by
-    one: chunk k's slot is k & turns, loaded `turns` chunks ahead."""
+    for the sixteen (each arrives for its own share). Its residual copy is asked for before
+    the wait for the products, or, with a pre-activation, after its store."""
     FULL = [sim.bar(f"full{i}", 3) for i in range(stages)]                 # CTA 0's
     EMPTY = [[sim.bar(f"empty{c}.{i}") for i in range(stages)] for c in range(2)]
     AFULL = [[sim.bar(f"afull{c}.{i}") for i in range(2)] for c in range(2)]
     AEMPTY = [sim.bar(f"aempty{i}", 2 * WARPS) for i in range(2)]          # CTA 0's
     DRAIN = [sim.bar(f"drain{c}") for c in range(2)]
-    RES = [[sim.bar(f"res{c}.{i}", 2) for i in range(2)] for c in range(2)]
+    RES = [sim.bar(f"res{c}", 2) for c in range(2)]
     members = [f"{r}{c}" for c in range(2) for r in ("producer", "mma", "epilogue")]
-    turns = 0 if pre else 1
 
     def producer(c):
         it = 0
@@ -63,24 +62,16 @@ def pair_roles(sim, units, stages=5, res=False, pre=False, chunks=2):
         yield ('named', 'cluster', members)
 
     def epilogue(c):
-        chunk = 0
-
-        def load(k):
-            yield ('arrive', RES[c][k & turns], 1, k >> turns)
-            yield ('tma', RES[c][k & turns], k >> turns)
-
         for lt in range(len(units)):
-            if res and turns:
-                yield from load(chunk)
+            load = [('arrive', RES[c], 1, lt), ('tma', RES[c], lt)]
+            if res and not pre:
+                yield from load
             yield ('wait', AFULL[c][lt & 1], lt >> 1)
-            for i in range(chunks):
-                if res and i + turns < chunks:
-                    yield from load(chunk + turns)
-                if i == chunks - 1:
-                    yield ('arrive', AEMPTY[lt & 1], WARPS)
-                if res:
-                    yield ('wait', RES[c][chunk & turns], chunk >> turns)
-                chunk += 1
+            if res:
+                if pre:
+                    yield from load
+                yield ('wait', RES[c], lt)
+            yield ('arrive', AEMPTY[lt & 1], WARPS)
         yield ('named', 'cluster', members)
 
     roles = {}
@@ -157,49 +148,32 @@ def test_tile_kernel_protocol(ksteps, stages):
         sim.run(tile_roles(sim, ksteps, stages))
 
 
-class Slots:
-    """A warp's bulk stores, each its own group, read from shared memory as late as the
-    waits allow: wait_read(n) forces all but the last n."""
-
-    def __init__(self):
-        self.pending = []  # slots of unread stores, oldest first
-
-    def store(self, slot):
-        self.pending.append(slot)
-
-    def wait_read(self, n):
-        self.pending = self.pending[len(self.pending) - n:] if n < len(self.pending) \
-            else self.pending
-
-    def write(self, slot):
-        assert slot not in self.pending, "a slot written while a store still reads it"
-
-
 @pytest.mark.parametrize("res,pre", list(itertools.product([False, True], repeat=2)))
-def test_staging_slots(res, pre):
-    """The epilogue's order of waits, residual loads, writes and stores over tiles with 0, 1
-    and 2 chunks inside."""
-    turns = 0 if pre else 1
-    s, chunk = Slots(), 0
-    for n in (2, 2, 1, 0, 2, 1, 1, 2, 0, 1, 2):
-        if res and turns and n > 0:
-            s.wait_read(1)
-            s.write(chunk & turns)  # residual load
-        for c in range(n):
-            s.wait_read(0 if res else 1)
-            if res and c + turns < n:
-                s.write((chunk + turns) & turns)
-            if pre:
-                s.write('pre')
-                s.store('pre')
-                if not res:
-                    s.wait_read(1)
-            if not (res and not turns):
-                s.write(chunk & turns)
-            elif res:
-                s.write(0)
-            s.store(chunk & turns)
-            chunk += 1
+def test_staging_slot(res, pre):
+    """The order of an epilogue warp's waits, residual loads, writes and stores over tiles
+    inside and outside, with every store read from the slot as late as the waits allow."""
+    unread = False  # a store that may still read the slot
+
+    def write():
+        assert not unread, "the slot written while a store still reads it"
+
+    for inside in (True, True, False, True, False, False, True, True):
+        if not inside:
+            continue
+        if res and not pre:
+            unread = False  # wait_group.read 0
+            write()         # the residual copy
+        if pre:
+            unread = False
+            write()
+            unread = True   # the pre-activation's store
+            if res:
+                unread = False
+                write()
+        if not res:
+            unread = False
+        write()             # the output, in place of the residual
+        unread = True
 
 
 def swizzle(row, units):
