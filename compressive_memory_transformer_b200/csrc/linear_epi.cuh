@@ -14,13 +14,6 @@ namespace infini {
 
 constexpr float kLog2e = 1.4426950408889634f;
 
-__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
-  uint64_t d;
-  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
-  return d;
-}
-__device__ __forceinline__ uint64_t both(float v) { return f2pack(v, v); }
-
 // 1 / x to about one unit in the last place; 0 for an infinite x.
 __device__ __forceinline__ float rcp_approx(float x) {
   float y;

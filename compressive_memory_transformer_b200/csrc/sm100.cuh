@@ -490,6 +490,12 @@ __device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
   asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
   return d;
 }
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+  uint64_t d;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
+__device__ __forceinline__ uint64_t both(float v) { return f2pack(v, v); }
 
 // 2^x for a pair of fp32 values on the FMA pipe (x <= 126; -inf allowed), so that
 // the MUFU unit is not the only pipe evaluating softmax exponentials.
