@@ -29,22 +29,27 @@ __device__ __forceinline__ uint64_t sigmoid_exp2(uint64_t t) {
   return f2pack(rcp_approx(a), rcp_approx(b));
 }
 
-// Phi(-z sqrt 2) = erfc(z) / 2 for z = az / sqrt 2 >= 0 and e = exp(-z^2), by Abramowitz
-// and Stegun, Handbook of Mathematical Functions, 7.1.26:
-// erfc(z) = t (a1 + t (a2 + ... a5)) exp(-z^2) + err, t = 1 / (1 + 0.3275911 z),
-// |err| <= 1.5e-7 (here halved), below the rounding of every result that it enters.
+// Phi(-az) of the normal distribution for az >= 0, and e = exp(-az^2 / 2): e t (c0 + c1 t + ...
+// + c7 t^7) with t = 1 / (1 + 0.306 az). The coefficients are a fit of this file's own, by
+// reweighted least squares against Phi(-az) / e over 0 <= az <= 14.5 for the least largest
+// relative error, 1.1e-7 (3.6e-7 evaluated in fp32). It is the relative error that counts:
+// for v < 0 gelu is -|v| Phi(-|v|) with nothing larger beside it. What e adds is az^2 2^-22
+// relative, 2^-16 at az = 8, far below the bf16 rounding of the result.
 __device__ __forceinline__ uint64_t normal_tail(uint64_t az, uint64_t& e) {
-  const uint64_t d = fma2(az, both(0.3275911f * 0.70710678f), both(1.f));
+  const uint64_t d = fma2(az, both(0.306f), both(1.f));
   const uint64_t x = mul2(mul2(az, az), both(-0.5f * kLog2e));
   float a, b;
   f2unpack(d, a, b);
   const uint64_t t = f2pack(rcp_approx(a), rcp_approx(b));
   f2unpack(x, a, b);
   e = f2pack(ex2_approx(a), ex2_approx(b));
-  uint64_t q = fma2(t, both(0.5f * 1.061405429f), both(0.5f * -1.453152027f));
-  q = fma2(t, q, both(0.5f * 1.421413741f));
-  q = fma2(t, q, both(0.5f * -0.284496736f));
-  q = fma2(t, q, both(0.5f * 0.254829592f));
+  uint64_t q = fma2(t, both(0.0365375690f), both(-0.150698826f));
+  q = fma2(t, q, both(0.179383233f));
+  q = fma2(t, q, both(-0.0330344550f));
+  q = fma2(t, q, both(0.118628532f));
+  q = fma2(t, q, both(0.104367673f));
+  q = fma2(t, q, both(0.122772224f));
+  q = fma2(t, q, both(0.122044101f));
   return mul2(mul2(t, q), e);
 }
 

@@ -1,0 +1,66 @@
+"""GPU tests of the linear layer where its first tests do not reach: activations far out on
+their negative side."""
+import math
+
+import pytest
+import torch
+
+import block_ref as ref
+from test_gpu_linear import BF, ia, ok  # noqa: F401
+
+pytestmark = pytest.mark.gpu
+
+
+def far_values(lo, hi):
+    """Every bf16 value from -hi to -lo."""
+    bits = torch.arange(0x10000, dtype=torch.int32).to(torch.int16).view(BF)
+    v = bits[torch.isfinite(bits) & (bits <= -lo) & (bits >= -hi)]
+    return v.sort().values
+
+
+def tail_error(v):
+    """Relative error that a normal tail Phi(-|v|) = exp(-v^2 / 2) q(|v|) may have in fp32:
+    2^-18 for q (a fit within 2^-20, its roundings and a reciprocal), and v^2 2^-22 for the
+    exponential, whose argument v^2 log2(e) / 2 has up to three roundings of 2^-24 relative,
+    times ln 2."""
+    return 2.0 ** -18 + v * v * 2.0 ** -22
+
+
+@pytest.mark.parametrize("rows,cols", [(40, 8), (400, 72), (4096, 1024)])
+def test_gelu_of_negative_values(ia, rows, cols):
+    """gelu(v) = -|v| Phi(-|v|) for v < 0: nothing larger stands beside the tail, so it has to
+    be right relative to itself. pre is one product with 1, exact."""
+    v = far_values(2.0, 13.0)
+    # all of them over and over, or as many as there are rows
+    pick = torch.arange(rows) % len(v) if rows >= len(v) else \
+        torch.linspace(0, len(v) - 1, rows).long()
+    v = v[pick].cuda()
+    x = torch.zeros(rows, 8, dtype=BF, device="cuda")
+    x[:, 0] = v
+    W = torch.zeros(8, cols, dtype=BF, device="cuda")
+    W[0] = 1.0
+    y, pre = ia.infini_attn_linear(x, W, act=ia.ACT_GELU, save_preact=True)
+    ok(ia)
+    assert torch.equal(pre, v[:, None].expand(rows, cols))
+    d = v.double()
+    want = -d.abs() * torch.erfc(d.abs() / math.sqrt(2)) / 2
+    bound = want.abs() * (ref.BF16 + tail_error(d)) + 2.0 ** -120
+    off = (y.double() - want[:, None]).abs() / bound[:, None]
+    assert float(off.max()) <= 1.0
+
+
+def test_gelu_derivative_of_negative_values(ia):
+    """gelu'(v) = Phi(v) + v phi(v), in fp32: with one row and dy = 1, dbias is act'(pre)."""
+    v = far_values(0.25, 12.0)
+    v = v[: len(v) // 8 * 8].cuda()
+    n = len(v)
+    one = torch.ones(1, n, dtype=BF, device="cuda")
+    _, _, got = ia.infini_attn_linear_backward(
+        torch.zeros(1, 8, dtype=BF, device="cuda"), torch.zeros(8, n, dtype=BF, device="cuda"),
+        one, act=ia.ACT_GELU, preact=v[None])
+    ok(ia)
+    d = v.double()
+    tail = torch.erfc(d.abs() / math.sqrt(2)) / 2
+    slope = d * torch.exp(-d * d / 2) / math.sqrt(2 * math.pi)
+    bound = (tail + slope.abs()) * tail_error(d) + 2.0 ** -120
+    assert float(((got.double() - (tail + slope)).abs() / bound).max()) <= 1.0
