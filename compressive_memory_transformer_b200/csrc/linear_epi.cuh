@@ -90,7 +90,8 @@ __device__ __forceinline__ void act_deriv_pair(float& a, float& b) {
     const uint64_t s = sigmoid_exp2(mul2(v, both(-kLog2e)));
     f2unpack(mul2(s, fma2(v, fma2(s, minus, one), one)), a, b);
   } else if constexpr (ACT == kActGeluTanh) {
-    const uint64_t q = mul2(v, v);
+    // s is 0 or 1 long before v^2 overflows; kept finite, so that 0 times du stays 0
+    const uint64_t q = f2pack(fminf(a * a, 1e30f), fminf(b * b, 1e30f));
     const uint64_t p = fma2(q, both(-0.071354816f * kLog2e), both(-1.5957691f * kLog2e));
     const uint64_t s = sigmoid_exp2(mul2(v, p));
     const uint64_t du = fma2(q, both(0.21406445f), both(1.5957691f));

@@ -1,5 +1,5 @@
 """GPU tests of the linear layer where its first tests do not reach: activations far out on
-their negative side."""
+their negative side and at huge values."""
 import math
 
 import pytest
@@ -64,3 +64,27 @@ def test_gelu_derivative_of_negative_values(ia):
     slope = d * torch.exp(-d * d / 2) / math.sqrt(2 * math.pi)
     bound = (tail + slope.abs()) * tail_error(d) + 2.0 ** -120
     assert float(((got.double() - (tail + slope)).abs() / bound).max()) <= 1.0
+
+
+@pytest.mark.parametrize("act", [1, 2, 3, 4])
+def test_huge_values(ia, act):
+    """Values whose squares overflow fp32: every activation here is v or 0 there, its
+    derivative 1 or 0."""
+    big = torch.tensor([100.0, 1e10, 1.8e19, 2e19, 1e20, 1e30, 3e38, 3.3e38])
+    v = torch.cat([big, -big]).to(BF).cuda()
+    x = torch.zeros(16, 8, dtype=BF, device="cuda")
+    x[:, 0] = v
+    W = torch.zeros(8, 8, dtype=BF, device="cuda")
+    W[0] = 1.0
+    y = ia.infini_attn_linear(x, W, act=act)
+    want = torch.where(v > 0, v, torch.zeros_like(v))[:, None].expand(16, 8)
+    assert bool((y == want).all())
+    for rows in (1, 2000):  # few rows and many take different kernels
+        dy = torch.ones(rows, 16, dtype=BF, device="cuda")
+        pre = v[None].expand(rows, 16).contiguous()
+        _, _, got = ia.infini_attn_linear_backward(
+            torch.zeros(rows, 8, dtype=BF, device="cuda"),
+            torch.zeros(8, 16, dtype=BF, device="cuda"), dy, act=act, preact=pre)
+        # sums of `rows` ones (or zeros) are exact in fp32
+        assert torch.equal(got, rows * (v > 0).float())
+    ok(ia)
