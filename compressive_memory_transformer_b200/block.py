@@ -167,7 +167,8 @@ def infini_attn_linear(x, W, bias=None, act=ACT_NONE, residual=None, save_preact
     """y = act(x W + bias) + residual: x [..., K], W [K, N], residual [..., N] bf16, bias [N]
     fp32; K and N multiples of 8. Returns y [..., N], and with save_preact (y, x W + bias),
     the second for the gradient of the activation. x, W, residual and out may be slices of
-    wider 2-d tensors (row strides a multiple of 8); out may be residual itself."""
+    wider 2-d tensors (row strides a multiple of 8), out a slice of the same one as x or residual
+    if it shares no column with them; out may be residual itself."""
     dev = x.get_device()
     M, K, ldx = _matrix("x", x, dev)
     _, N, ldw = _weight(W, dev, K)

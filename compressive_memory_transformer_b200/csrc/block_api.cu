@@ -21,16 +21,24 @@ size_t up256(size_t x) { return (x + 255) & ~(size_t)255; }
 
 bool aligned(const void* p, size_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
 
-// A range of memory that a call reads or writes.
+// What a call reads or writes: n bytes from p, or (pitch > 0) rows of `width` bytes, `pitch`
+// bytes apart, that end within n bytes.
 struct Range {
   const void* p;
   size_t n;
+  size_t width = 0, pitch = 0;
 };
 
+// Two ranges with a byte in common. Rows of one pitch are apart where their columns are, as
+// slices of one wide array beside each other; other pitches are judged by the whole span.
 bool overlap(const Range& a, const Range& b) {
   if (!a.p || !b.p || a.n == 0 || b.n == 0) return false;
   const uintptr_t x = reinterpret_cast<uintptr_t>(a.p), y = reinterpret_cast<uintptr_t>(b.p);
-  return x < y + b.n && y < x + a.n;
+  if (x >= y + b.n || y >= x + a.n) return false;
+  if (a.pitch == 0 || a.pitch != b.pitch) return true;
+  // where b's rows start between the starts of a's
+  const size_t at = x <= y ? (y - x) % a.pitch : (a.pitch - (x - y) % a.pitch) % a.pitch;
+  return at < a.width || at + b.width > a.pitch;
 }
 
 // Every output apart from the inputs and the other outputs.
@@ -121,8 +129,10 @@ long long row_stride(long long ld, long long cols) {
   return ld < cols || ld % 8 != 0 || ld > kMaxLd ? -1 : ld;
 }
 
-size_t span(long long rows, long long cols, long long ld) {
-  return rows > 0 ? ((size_t)(rows - 1) * (size_t)ld + (size_t)cols) * 2 : 0;
+// A bf16 matrix of `rows` rows, ld elements apart.
+Range matrix(const void* p, long long rows, long long cols, long long ld) {
+  const size_t width = (size_t)cols * 2, pitch = (size_t)ld * 2;
+  return {p, rows > 0 ? (size_t)(rows - 1) * pitch + width : 0, width, pitch};
 }
 
 int linear_sizes(long long M, int K, int N, int act) {
@@ -145,11 +155,10 @@ int linear_impl(const infini_attn_linear_t* p, cudaStream_t stream) {
     if (!aligned(q, 16)) return INFINI_ERR_ALIGN;
   // the residual may be y itself: every element is read by the thread that then writes it
   const bool in_place = p->residual == p->y && ldr == ldy;
-  const Range in[4] = {{p->x, span(p->M, p->K, ldx)},
-                       {p->W, span(p->K, p->N, ldw)},
+  const Range in[4] = {matrix(p->x, p->M, p->K, ldx), matrix(p->W, p->K, p->N, ldw),
                        {p->bias, (size_t)p->N * 4},
-                       {in_place ? nullptr : p->residual, span(p->M, p->N, ldr)}};
-  const Range out[2] = {{p->y, span(p->M, p->N, ldy)}, {p->preact, span(p->M, p->N, ldp)}};
+                       matrix(in_place ? nullptr : p->residual, p->M, p->N, ldr)};
+  const Range out[2] = {matrix(p->y, p->M, p->N, ldy), matrix(p->preact, p->M, p->N, ldp)};
   if (aliased(in, 4, out, 2)) return INFINI_ERR_ALIAS;
   if (p->M == 0) return INFINI_OK;
   int sms = 0;
@@ -209,12 +218,10 @@ int linear_backward_impl(const infini_attn_linear_grad_t* p, const infini_attn_o
   for (const void* q : {p->x, p->W, p->preact, p->dy, static_cast<const void*>(p->dx),
                         static_cast<const void*>(p->dW), static_cast<const void*>(p->dbias)})
     if (!aligned(q, 16)) return INFINI_ERR_ALIGN;
-  const Range in[4] = {{p->x, span(p->M, p->K, ldx)},
-                       {p->W, span(p->K, p->N, ldw)},
-                       {act ? p->preact : nullptr, span(p->M, p->N, ldp)},
-                       {p->dy, span(p->M, p->N, lddy)}};
-  const Range out[3] = {{p->dx, span(p->M, p->K, lddx)},
-                        {p->dW, span(p->K, p->N, lddw)},
+  const Range in[4] = {matrix(p->x, p->M, p->K, ldx), matrix(p->W, p->K, p->N, ldw),
+                       matrix(act ? p->preact : nullptr, p->M, p->N, ldp),
+                       matrix(p->dy, p->M, p->N, lddy)};
+  const Range out[3] = {matrix(p->dx, p->M, p->K, lddx), matrix(p->dW, p->K, p->N, lddw),
                         {p->dbias, (size_t)p->N * 4}};
   if (aliased(in, 4, out, 3)) return INFINI_ERR_ALIAS;
   int sms = 0;

@@ -380,7 +380,9 @@ typedef enum {
  * Products are summed in fp32; bias, activation and residual are applied in fp32 and y
  * (and preact) rounded once. M >= 0 (0: nothing to do), K and N multiples of 8
  * (INFINI_ERR_UNSUPPORTED otherwise), M < 2^31; every pointer 16-byte aligned; y and preact
- * may not overlap each other or an input (but for residual == y). No scratch. The result
+ * may not overlap each other or an input (but for residual == y). Matrices with one row stride
+ * may be columns of one wide array beside each other; with different strides their whole
+ * address ranges have to be apart. No scratch. The result
  * depends on the sizes and the device only (fixed order of every sum).
  */
 typedef struct {

@@ -1,12 +1,12 @@
 """GPU tests of the linear layer where its first tests do not reach: activations far out on
-their negative side and at huge values."""
+their negative side and at huge values, slices of one wide array."""
 import math
 
 import pytest
 import torch
 
 import block_ref as ref
-from test_gpu_linear import BF, ia, ok  # noqa: F401
+from test_gpu_linear import BF, ia, normal, ok  # noqa: F401
 
 pytestmark = pytest.mark.gpu
 
@@ -88,3 +88,28 @@ def test_huge_values(ia, act):
         # sums of `rows` ones (or zeros) are exact in fp32
         assert torch.equal(got, rows * (v > 0).float())
     ok(ia)
+
+
+@pytest.mark.parametrize("M", [1, 40, 700, 2600])
+def test_slices_of_one_array(ia, M):
+    """x, the residual and the output as columns of one array: results as from arrays of
+    their own, and the other columns stay as they were."""
+    K, N = 200, 1096
+    wide = normal((M, 8 + K + N + N + 16), 1)
+    x, r, y = wide[:, 8:8 + K], wide[:, 8 + K:8 + K + N], wide[:, 16 + K + N:16 + K + 2 * N]
+    W, b = normal((K, N), 2, K ** -0.5), normal((N,), 3, 0.5, torch.float32)
+    kw = dict(bias=b, act=ia.ACT_SILU)
+    want = ia.infini_attn_linear(x.contiguous(), W, residual=r.contiguous(), **kw)
+    before = wide.clone()
+    ia.infini_attn_linear(x, W, residual=r, out=y, **kw)
+    ok(ia)
+    assert torch.equal(y, want)
+    y.copy_(before[:, 16 + K + N:16 + K + 2 * N])
+    assert torch.equal(wide, before)
+    ia.infini_attn_linear(x, W, residual=r, out=r, **kw)
+    ok(ia)
+    assert torch.equal(r, want)
+    r.copy_(before[:, 8 + K:8 + K + N])
+    assert torch.equal(wide, before)
+    with pytest.raises(ia.InfiniError):  # eight columns of the residual
+        ia.infini_attn_linear(x, W, residual=r, out=wide[:, K + N:K + 2 * N], **kw)
