@@ -495,6 +495,25 @@ BlockPlan block_plan(int B, long long L, int D_model, int D_ff, int H, int H_kv,
           up256(infini_attn_layer_workspace_size(B, L, D_model, H, H_kv, N, d, mode))};
 }
 
+// The sizes that the block takes, for the call and for its scratch query.
+int block_sizes(int B, long long L, int D_model, int D_ff, int H, int H_kv, int N, int d,
+                int mode) {
+  if (B < 1 || L < 1 || D_model < 1 || D_ff < 1 || H < 1 || H_kv < 1 || N < 1 || H % H_kv != 0 ||
+      L >= (1ll << 31) / B)
+    return INFINI_ERR_SHAPE;
+  const long long tokens = B * L;
+  int st = linear_sizes(tokens, D_model, D_ff, INFINI_ACT_NONE);
+  if (st != INFINI_OK) return st;
+  if ((st = norm_sizes(tokens, D_model, INFINI_NORM_RMS, INFINI_DTYPE_BF16, 0.f)) != INFINI_OK)
+    return st;
+  if ((mode != INFINI_LINEAR && mode != INFINI_DELTA) || d != 128 || D_model % 128 != 0 ||
+      tokens % 128 != 0)
+    return INFINI_ERR_UNSUPPORTED;
+  return infini_attn_layer_workspace_size(B, L, D_model, H, H_kv, N, d, mode) == 0
+             ? INFINI_ERR_SHAPE
+             : INFINI_OK;
+}
+
 // Everything that the block's steps would refuse, before the first launch.
 int block_checks(const infini_attn_block_t* p) {
   if (!p || !p->x || !p->y || !p->Wq || !p->Wk || !p->Wv || !p->Wo || !p->beta ||
@@ -504,25 +523,17 @@ int block_checks(const infini_attn_block_t* p) {
       (p->M_out == nullptr) != (p->z_out == nullptr) ||
       (p->attn_post_norm_bias && !p->attn_post_norm) || (p->mlp_post_norm_bias && !p->mlp_post_norm))
     return INFINI_ERR_NULL;
-  if (p->B < 1 || p->L < 1 || p->D_model < 1 || p->D_ff < 1 || p->H < 1 || p->H_kv < 1 ||
-      p->N < 1 || p->H % p->H_kv != 0 || p->L >= (1ll << 31) / p->B)
-    return INFINI_ERR_SHAPE;
-  const long long tokens = p->B * p->L;
-  int st = linear_sizes(tokens, p->D_model, p->D_ff, p->act);
+  int st = block_sizes(p->B, p->L, p->D_model, p->D_ff, p->H, p->H_kv, p->N, p->d, p->mode);
   if (st != INFINI_OK) return st;
+  const long long tokens = p->B * p->L;
+  if ((st = linear_sizes(tokens, p->D_model, p->D_ff, p->act)) != INFINI_OK) return st;
   if ((st = norm_sizes(tokens, p->D_model, p->kind, INFINI_DTYPE_BF16, p->eps)) != INFINI_OK)
     return st;
-  if ((p->mode != INFINI_LINEAR && p->mode != INFINI_DELTA) || p->d != 128 ||
-      p->D_model % 128 != 0 || tokens % 128 != 0)
-    return INFINI_ERR_UNSUPPORTED;
   if (p->kind == INFINI_NORM_RMS && (p->attn_norm_bias || p->attn_post_norm_bias ||
                                      p->mlp_norm_bias || p->mlp_post_norm_bias))
     return INFINI_ERR_UNSUPPORTED;
   if ((p->attn_gate || p->mlp_gate) &&
       (p->gate_groups < 1 || p->gate_groups > tokens || tokens % p->gate_groups != 0))
-    return INFINI_ERR_SHAPE;
-  if (infini_attn_layer_workspace_size(p->B, p->L, p->D_model, p->H, p->H_kv, p->N, p->d,
-                                       p->mode) == 0)
     return INFINI_ERR_SHAPE;
   for (const void* q : {p->x, p->Wq, p->Wk, p->Wv, p->Wo, p->W_up, p->W_down,
                         static_cast<const void*>(p->y), static_cast<const void*>(p->b_up),
@@ -726,9 +737,8 @@ int infini_attn_block_forward(const infini_attn_block_t* p, const infini_attn_op
 
 size_t infini_attn_block_workspace_size(int B, long long L, int D_model, int D_ff, int H,
                                         int H_kv, int N, int d, int mode) {
-  if (B < 1 || L < 1 || D_model < 1 || D_ff < 1 || L > (1ll << 31) / B) return 0;
-  const BlockPlan f = block_plan(B, L, D_model, D_ff, H, H_kv, N, d, mode);
-  return f.layer ? f.bytes() : 0;
+  if (block_sizes(B, L, D_model, D_ff, H, H_kv, N, d, mode) != INFINI_OK) return 0;
+  return block_plan(B, L, D_model, D_ff, H, H_kv, N, d, mode).bytes();
 }
 
 }  // extern "C"

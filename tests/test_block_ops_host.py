@@ -1,5 +1,6 @@
 """Host side of the operators around the attention layer that needs no GPU: which
-neighbouring slices of one wide array a call may take."""
+neighbouring slices of one wide array a call may take, the scratch sizes of sizes that are
+refused."""
 import ctypes
 
 import pytest
@@ -82,3 +83,13 @@ def test_shared_columns_are_refused(ia):
                dict(residual=at(64), y=at(72), preact=at(320)),
                dict(y=at(192), ldy=520)):
         assert linear(ia, **{**ld, **kw}) == ALIAS
+
+
+@pytest.mark.parametrize("kw", [
+    dict(D_model=192), dict(D_model=8320), dict(D_ff=12), dict(mode=3), dict(mode=-1),
+    dict(L=100), dict(d=64), dict(H=3, H_kv=2), dict(N=0), dict(B=0), dict(L=1 << 31)])
+def test_block_scratch_of_unsupported_sizes_is_zero(ia, kw):
+    a = dict(B=1, L=128, D_model=256, D_ff=512, H=2, H_kv=1, N=128, d=128, mode=0)
+    assert ia.block_workspace_size(**a) > 0
+    a.update(kw)
+    assert ia.block_workspace_size(**a) == 0
