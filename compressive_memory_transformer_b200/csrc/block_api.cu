@@ -227,11 +227,14 @@ int linear_backward_impl(const infini_attn_linear_grad_t* p, const infini_attn_o
   int sms = 0;
   if ((st = prepare(&sms)) != INFINI_OK) return st;
   if (p->M == 0) {  // sums over no rows
+    record(opts, 0, stream);
+    if (p->dbias && cudaMemsetAsync(p->dbias, 0, (size_t)p->N * 4, stream) != cudaSuccess)
+      return INFINI_ERR_CUDA;
+    record(opts, 1, stream);
     if (p->dW && cudaMemset2DAsync(p->dW, (size_t)lddw * 2, 0, (size_t)p->N * 2, (size_t)p->K,
                                    stream) != cudaSuccess)
       return INFINI_ERR_CUDA;
-    if (p->dbias && cudaMemsetAsync(p->dbias, 0, (size_t)p->N * 4, stream) != cudaSuccess)
-      return INFINI_ERR_CUDA;
+    record(opts, 2, stream);
     return INFINI_OK;
   }
   const GradPlan f = grad_plan(p->M, p->K, p->N, p->act, p->dbias != nullptr, p->dx != nullptr,

@@ -1,5 +1,6 @@
 """GPU tests of the linear layer where its first tests do not reach: activations far out on
-their negative side and at huge values, slices of one wide array."""
+their negative side and at huge values, slices of one wide array, an empty batch's
+events."""
 import math
 
 import pytest
@@ -113,3 +114,20 @@ def test_slices_of_one_array(ia, M):
     assert torch.equal(wide, before)
     with pytest.raises(ia.InfiniError):  # eight columns of the residual
         ia.infini_attn_linear(x, W, residual=r, out=wide[:, K + N:K + 2 * N], **kw)
+
+
+def test_events_of_an_empty_batch(ia):
+    """The stage events are recorded for no rows too."""
+    ev = [torch.cuda.Event(enable_timing=True) for _ in range(3)]
+    for e in ev:
+        e.record()
+    busy = normal((4096, 4096), 1, dtype=torch.float32)
+    for _ in range(4):
+        busy = busy * 0.5
+    mark = torch.cuda.Event(enable_timing=True)
+    mark.record()
+    x, W, dy = normal((0, 64), 1), normal((64, 32), 2), normal((0, 32), 3)
+    ia.infini_attn_linear_backward(x, W, dy, stage_events=ev)
+    torch.cuda.synchronize()
+    times = [mark.elapsed_time(e) for e in ev]
+    assert 0 <= times[0] <= times[1] <= times[2]
