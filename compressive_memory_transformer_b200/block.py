@@ -5,7 +5,8 @@ rest of the package; the names are those of include/infini_attn.h.
 
 Every call runs on the device of its tensors: on `stream`, or on that device's current
 stream. Outputs and scratch that a call makes come from torch's allocator on the same
-stream. Inputs made on another stream have to be ready (an event, a wait) by then.
+stream. Inputs made on another stream have to be ready (an event, a wait) by then, and every
+tensor of a call has to stay until the call's work on its stream is done.
 """
 from __future__ import annotations
 
@@ -85,20 +86,17 @@ for _name, (_res, _args) in SIGS.items():
     _fn.restype = _res
 
 
-_current_device = torch._C._cuda_getDevice
-_current_stream = torch._C._cuda_getCurrentRawStream
-
-
 def _on(dev, stream, call):
     """call(stream handle) with the device and the stream current, so that what it allocates
     belongs to the stream that it runs on. (The usual case, no stream given and the
     tensors' device already current, takes no context manager: they cost more than a small
-    call's kernels.)"""
+    call's kernels. torch._C's functions are looked up here: a torch built without CUDA has
+    none, and still imports this package.)"""
     if stream is None:
-        if dev == _current_device():
-            return call(_current_stream(dev))
+        if dev == torch._C._cuda_getDevice():
+            return call(torch._C._cuda_getCurrentRawStream(dev))
         with torch.cuda.device(dev):
-            return call(_current_stream(dev))
+            return call(torch._C._cuda_getCurrentRawStream(dev))
     if stream.device_index != dev:
         raise ValueError("the stream is on another device than the tensors")
     with torch.cuda.device(dev), torch.cuda.stream(stream):

@@ -1,13 +1,17 @@
 """Host side of the operators around the attention layer that needs no GPU: which
 neighbouring slices of one wide array a call may take, the scratch sizes of sizes that are
-refused."""
+refused, and the import without torch's CUDA build."""
 import ctypes
+import os
+import subprocess
+import sys
 
 import pytest
 
 CUDA, NOMEM, ALIAS = -5, -6, -8
 FAKE = 1 << 20  # aligned addresses that are never read
 MB = 1 << 24
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
 
 
 @pytest.fixture(scope="module")
@@ -93,3 +97,16 @@ def test_block_scratch_of_unsupported_sizes_is_zero(ia, kw):
     assert ia.block_workspace_size(**a) > 0
     a.update(kw)
     assert ia.block_workspace_size(**a) == 0
+
+
+def test_import_without_torchs_cuda_build(ia):
+    """A torch built without CUDA lacks torch._C's CUDA functions: the package still imports
+    (its host checks, sizes and error texts need no GPU)."""
+    code = ("import torch\n"
+            "for n in [n for n in dir(torch._C) if n.startswith('_cuda_')]:\n"
+            "    delattr(torch._C, n)\n"
+            "import compressive_memory_transformer_b200 as ia\n"
+            "assert ia.linear_backward_workspace_size(64, 64, 64) >= 0\n")
+    r = subprocess.run([sys.executable, "-c", code], cwd=ROOT, capture_output=True, text=True,
+                       timeout=300)
+    assert r.returncode == 0, r.stderr[-2000:]
