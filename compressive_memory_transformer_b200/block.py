@@ -275,10 +275,10 @@ def _norm_args(x, b, gate, alpha, post_weight, post_bias, pre_weight, pre_bias, 
         _vector("post_bias", post_bias, D, dev)
         a.pre_bias, a.post_bias = _p(pre_bias), _p(post_bias)
     if gate is not None:
-        if gate.dim() not in (1, 2) or gate.shape[-1] != D or gate.shape[0] == 0:
+        if gate.dim() not in (1, 2) or gate.shape[-1] != D:
             raise ValueError("gate must be [dim] or [groups, dim]")
         groups = gate.shape[0] if gate.dim() == 2 else 1
-        if rows % groups:
+        if rows % groups if groups else rows:  # no groups: a row per token of no tokens
             raise ValueError("gate's groups must divide the rows")
         _vector("gate", gate, groups * D, dev)
         a.gate, a.gate_groups = gate.data_ptr(), groups

@@ -320,8 +320,10 @@ int norm_parts(const infini_attn_residual_norm_t* p) {
   if (p->rows > 0 && !p->b && (p->gate || p->post_weight)) return INFINI_ERR_NULL;
   if ((p->pre_bias && !p->pre_weight) || (p->post_bias && !p->post_weight)) return INFINI_ERR_NULL;
   if (p->kind == INFINI_NORM_RMS && (p->pre_bias || p->post_bias)) return INFINI_ERR_UNSUPPORTED;
-  if (p->gate && (p->gate_groups < 1 || p->gate_groups > (1ll << 31) ||
-                  p->rows % p->gate_groups != 0))
+  // a gate row per token of no tokens is no gate row
+  const bool no_gate_rows = p->rows == 0 && p->gate_groups == 0;
+  if (p->gate && !no_gate_rows && (p->gate_groups < 1 || p->gate_groups > (1ll << 31) ||
+                                   p->rows % p->gate_groups != 0))
     return INFINI_ERR_SHAPE;
   const size_t e = p->dtype == INFINI_DTYPE_BF16 ? 2 : 4;
   for (const void* q : {p->x, p->b})
@@ -342,7 +344,7 @@ NormArgs norm_args(const infini_attn_residual_norm_t* p) {
   a.pre_w = p->pre_weight;
   a.pre_b = p->pre_bias;
   a.rows = p->rows;
-  a.groups = p->gate ? p->gate_groups : 1;
+  a.groups = p->gate && p->gate_groups > 0 ? p->gate_groups : 1;
   a.group_rows = p->rows / a.groups;
   a.D = p->dim;
   a.alpha = p->alpha;
@@ -453,8 +455,8 @@ int residual_norm_backward_impl(const infini_attn_residual_norm_t* p,
     if (norm_backward_launch(a, p->kind, p->dtype == INFINI_DTYPE_F32, f.blocks, stream) !=
         cudaSuccess)
       return INFINI_ERR_CUDA;
-  } else if (g->dgate && cudaMemsetAsync(g->dgate, 0, nv * (size_t)a.groups, stream) !=
-                             cudaSuccess) {
+  } else if (g->dgate && p->gate_groups > 0 &&
+             cudaMemsetAsync(g->dgate, 0, nv * (size_t)p->gate_groups, stream) != cudaSuccess) {
     return INFINI_ERR_CUDA;
   }
   const bool gates = p->rows > 0 && f.gpart;

@@ -444,7 +444,7 @@ typedef enum { INFINI_NORM_RMS = 0, INFINI_NORM_LAYER = 1 } infini_norm_t;
  *                may be NULL (not written); each may be x or b itself, but no other overlap.
  *   gate         fp32 [gate_groups][dim] or NULL; row i takes gate row
  *                i / (rows / gate_groups): 1 group gates all rows alike, one per batch entry
- *                gates each sequence, `rows` groups gate each token
+ *                gates each sequence, `rows` groups gate each token (0 of 0 rows too)
  *   post_*, pre_*  fp32 [dim]; a norm is there when its weight is, its bias (layer norm
  *                only) may be NULL
  * rows >= 0; 1 <= dim <= 8192 (INFINI_ERR_UNSUPPORTED beyond); eps >= 0. No alignment beyond

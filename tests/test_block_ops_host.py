@@ -1,6 +1,6 @@
 """Host side of the operators around the attention layer that needs no GPU: which
 neighbouring slices of one wide array a call may take, the scratch sizes of sizes that are
-refused, and the import without torch's CUDA build."""
+refused, empty gates, and the import without torch's CUDA build."""
 import ctypes
 import os
 import subprocess
@@ -8,7 +8,7 @@ import sys
 
 import pytest
 
-CUDA, NOMEM, ALIAS = -5, -6, -8
+SHAPE, CUDA, NOMEM, ALIAS = -2, -5, -6, -8
 FAKE = 1 << 20  # aligned addresses that are never read
 MB = 1 << 24
 ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
@@ -97,6 +97,21 @@ def test_block_scratch_of_unsupported_sizes_is_zero(ia, kw):
     assert ia.block_workspace_size(**a) > 0
     a.update(kw)
     assert ia.block_workspace_size(**a) == 0
+
+
+def test_a_gate_row_per_token_of_no_tokens(ia):
+    """`rows` gate groups are allowed, 0 rows too; with rows there has to be a group."""
+    from compressive_memory_transformer_b200.block import ResidualNormArgs, ResidualNormGradArgs
+    a = dict(x=FAKE, b=FAKE + MB, gate=FAKE + 2 * MB, pre_weight=FAKE + 4 * MB, r=FAKE + 5 * MB,
+             h=FAKE + 6 * MB, rows=0, gate_groups=0, dim=128, kind=0, dtype=0, alpha=1.0, eps=1e-5)
+    call = lambda: ia.raw_call("infini_attn_residual_norm", ctypes.byref(ResidualNormArgs(**a)),
+                               None)
+    assert call() == 0
+    a["rows"] = 4
+    assert call() == SHAPE
+    g = ResidualNormGradArgs(dr=FAKE + 7 * MB, dgate=FAKE + 8 * MB)
+    assert ia.raw_call("infini_attn_residual_norm_backward", ctypes.byref(ResidualNormArgs(**a)),
+                       ctypes.byref(g), None, None) == SHAPE
 
 
 def test_import_without_torchs_cuda_build(ia):

@@ -1,0 +1,21 @@
+"""GPU tests of the norms: gates of an empty batch."""
+import pytest
+import torch
+
+from test_gpu_norm import ia, normal  # noqa: F401
+
+pytestmark = pytest.mark.gpu
+
+
+def test_a_gate_row_per_token_of_no_tokens(ia):
+    """gate [rows, dim] of an empty batch: empty results, zero sums."""
+    x, b, gate = normal((0, 64), 1), normal((0, 64), 2), normal((0, 64), 3)
+    w = normal((64,), 4)
+    r, h = ia.infini_attn_residual_norm(x, b, gate=gate, pre_weight=w)
+    assert r.shape == h.shape == (0, 64)
+    got = ia.infini_attn_residual_norm_backward(x, b, x, x, gate=gate, pre_weight=w)
+    torch.cuda.synchronize()
+    assert got.dx.shape == got.db.shape == got.dgate.shape == (0, 64)
+    assert not bool(got.dpre_weight.any())
+    with pytest.raises(ValueError):
+        ia.infini_attn_residual_norm(w[None], w[None], gate=gate)
