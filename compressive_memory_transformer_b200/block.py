@@ -412,7 +412,7 @@ def infini_attn_block_forward(x, Wq, Wk, Wv, Wo, beta, N, mode, H, W_up, W_down,
     for name, t in (("attn_gate", attn_gate), ("mlp_gate", mlp_gate)):
         if t is not None:
             n = t.shape[0] if t.dim() == 2 else 1
-            if t.dim() not in (1, 2) or groups not in (0, n):
+            if t.dim() not in (1, 2) or n == 0 or groups not in (0, n):
                 raise ValueError("gates must be [D_model] or [groups, D_model], both alike")
             groups = n
             _vector(name, t, n * D, dev)

@@ -19,3 +19,14 @@ def test_a_gate_row_per_token_of_no_tokens(ia):
     assert not bool(got.dpre_weight.any())
     with pytest.raises(ValueError):
         ia.infini_attn_residual_norm(w[None], w[None], gate=gate)
+
+
+def test_block_refuses_a_gate_without_rows(ia):
+    """A gate of no groups for a block with tokens is refused, not left out."""
+    from test_gpu_block import block_case
+    p = block_case(1, 128, 128, 264, 1, 1, 0, 0, False)
+    none = torch.empty((0, 128), device="cuda")
+    for gates in (dict(attn_gate=none), dict(mlp_gate=none),
+                  dict(attn_gate=none, mlp_gate=torch.ones((1, 128), device="cuda"))):
+        with pytest.raises(ValueError):
+            ia.infini_attn_block_forward(**p, **gates)
