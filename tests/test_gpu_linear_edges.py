@@ -1,13 +1,13 @@
 """GPU tests of the linear layer where its first tests do not reach: activations far out on
-their negative side and at huge values, slices of one wide array, an empty batch's
-events."""
+their negative side and at huge values, slices of one wide array, an empty batch's events,
+and products whose reduction is split over pairs of SMs."""
 import math
 
 import pytest
 import torch
 
 import block_ref as ref
-from test_gpu_linear import BF, ia, normal, ok  # noqa: F401
+from test_gpu_linear import BF, ia, inputs, normal, ok  # noqa: F401
 
 pytestmark = pytest.mark.gpu
 
@@ -131,3 +131,30 @@ def test_events_of_an_empty_batch(ia):
     torch.cuda.synchronize()
     times = [mark.elapsed_time(e) for e in ev]
     assert 0 <= times[0] <= times[1] <= times[2]
+
+
+# parts of the reduction per pair of SMs in dW or dx, by the scratch that they need: the
+# partial tiles are fp32. Ragged in all three sizes; 6 parts of 98 k-steps are uneven.
+@pytest.mark.parametrize("M,K,N,of", [(8192, 1024, 1024, "dW"), (6838, 616, 1120, "dW"),
+                                      (6266, 2808, 216, "dW"), (40000, 512, 512, "dW"),
+                                      (1513, 928, 3200, "dx")])
+@pytest.mark.parametrize("act", [0, 2])
+def test_reduction_split_over_pairs(ia, M, K, N, of, act):
+    size = ia.linear_backward_workspace_size(M, K, N, act)
+    outputs = K * N if of == "dW" else M * K
+    d_bytes = 2 * M * N + 256 if act else 0
+    bias_parts = 4 * 450 * N if M > 1024 else 0  # a row of dbias per chunk at most
+    assert size > d_bytes + bias_parts + 2 * 4 * outputs * 0.99, "the case is not split any more"
+    room = torch.full((size + 4096,), 0xA5, dtype=torch.uint8, device="cuda")
+    x, W, _, _ = inputs(M, K, N, 80)
+    dy, pre = normal((M, N), 85, 1.0 / M), normal((M, N), 86, 2.0)
+    run = lambda ws: ia.infini_attn_linear_backward(x, W, dy, act=act, preact=pre if act else None,
+                                                    workspace=ws)
+    got = run(room[:size])
+    ok(ia)
+    assert bool((room[size:] == 0xA5).all())
+    for name, g, (r, e), step in zip(("dx", "dW", "dbias"), got,
+                                     ref.linear_backward(x, W, pre, dy, act),
+                                     (ref.BF16, ref.BF16, ref.F32)):
+        ref.within(g, r, e, step, name)
+    assert all(torch.equal(p, q) for p, q in zip(got, run(None)))
