@@ -197,8 +197,8 @@ GradPlan grad_plan(long long M, int K, int N, int act, bool dbias, bool dx, bool
   f.chunks = act_grad_chunks(M, N, sms);
   if (act != INFINI_ACT_NONE) f.dpre = up256((size_t)M * N * 2);
   if (dbias && f.chunks > 1) f.part = up256((size_t)f.chunks * N * 4);
-  const size_t a = dx ? linear_gemm_scratch(M, K, N, true, sms) : 0;
-  const size_t b = dW ? linear_gemm_scratch(K, N, M, true, sms) : 0;
+  const size_t a = dx ? linear_gemm_scratch(M, K, N, sms) : 0;
+  const size_t b = dW ? linear_gemm_scratch(K, N, M, sms) : 0;
   f.gemm = up256(a > b ? a : b);
   return f;
 }

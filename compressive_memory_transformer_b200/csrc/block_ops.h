@@ -32,8 +32,9 @@ struct GemmArgs {
 };
 
 cudaError_t linear_set_attributes();
-// Scratch of one product (0 for most shapes).
-size_t linear_gemm_scratch(long long P, long long Q, long long R, bool plain, int sms);
+// Scratch of one plain product, without bias, activation, residual or pre-activation (0 for
+// most shapes). With it a launch may split the reduction over pairs of SMs.
+size_t linear_gemm_scratch(long long P, long long Q, long long R, int sms);
 cudaError_t linear_gemm_launch(const GemmArgs& g, void* scratch, int sms, cudaStream_t stream);
 
 // dpre = dy * act'(pre) (bf16, only with act != none) and the column sums of the

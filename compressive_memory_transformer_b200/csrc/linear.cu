@@ -383,7 +383,7 @@ struct PairParams {
   int ksteps, split;
   long long rows, cols;
   Epilogue epi;    // out, res and pre go through tensor maps
-  float* partial;  // split > 1: [split][rows][cols]
+  float* partial;  // split > 1 (plain products): [split][rows][cols]
 };
 
 struct PairMaps {
@@ -595,7 +595,7 @@ linear_pair_kernel(const __grid_constant__ CUtensorMap tm_a,
     uint8_t* slot = staging + warp * kSlot;
     const uint32_t so = smem_u32(slot);
     uint64_t* rbar = &bars[Q_RES + warp];
-    const bool res = has_res && p.split == 1, bias = p.epi.bias && p.split == 1;
+    const bool res = has_res, bias = p.epi.bias != nullptr;
     int lt = 0, loads = 0;  // residual copies asked for; every one but the last waited for
     auto pack32 = [&](int half, const float (&v)[32]) {
 #pragma unroll
@@ -746,11 +746,11 @@ linear_pair_kernel(const __grid_constant__ CUtensorMap tm_a,
   }
 }
 
-// out from the partial sums of a split reduction, added in order, with the epilogue.
-// HBM- or L2-bound; a thread has 8 neighbouring columns.
+// out from the partial sums of a split reduction, added in order. HBM- or L2-bound; a thread
+// has 8 neighbouring columns.
 __global__ void __launch_bounds__(256)
 split_reduce_kernel(const float* __restrict__ partial, int split, long long rows, long long cols,
-                    const Epilogue epi) {
+                    __nv_bfloat16* __restrict__ out, long long ldo) {
   const long long units = rows * (cols / 8), per = cols / 8;
   for (long long u = blockIdx.x * 256ll + threadIdx.x; u < units; u += gridDim.x * 256ll) {
     const long long row = u / per, col = 8 * (u % per);
@@ -762,7 +762,7 @@ split_reduce_kernel(const float* __restrict__ partial, int split, long long rows
       v[0] += x.x; v[1] += x.y; v[2] += x.z; v[3] += x.w;
       v[4] += y.x; v[5] += y.y; v[6] += y.z; v[7] += y.w;
     }
-    finish8(v, epi, row, col);
+    *reinterpret_cast<uint4*>(out + row * ldo + col) = pack8(v);
   }
 }
 
@@ -869,7 +869,7 @@ cudaError_t pair_launch(const GemmArgs& g, int split, float* partial, int sms,
   if (e != cudaSuccess || split == 1) return e;
   const long long blocks = (g.P * (g.Q / 8) + 255) / 256;
   split_reduce_kernel<<<(unsigned)(blocks < 16ll * sms ? blocks : 16ll * sms), 256, 0, stream>>>(
-      partial, split, g.P, g.Q, p.epi);
+      partial, split, g.P, g.Q, g.out, g.ldo);
   return cudaGetLastError();
 }
 
@@ -985,7 +985,8 @@ int tile_split(int bn, long long tiles, long long ksteps, int sms) {
   return best;
 }
 
-// The fastest by the estimates (scratch: whether a split over pairs is possible).
+// The fastest by the estimates. A split over pairs needs scratch and is for plain products: the
+// gradients', whose reductions are long and whose tiles are few.
 GemmPlan gemm_plan(long long P, long long Q, long long R, bool scratch, int sms) {
   const long long ksteps = (R + kKStep - 1) / kKStep;
   const long long big = (P + 255) / 256 * ((Q + 255) / 256);
@@ -1006,8 +1007,8 @@ GemmPlan gemm_plan(long long P, long long Q, long long R, bool scratch, int sms)
 
 }  // namespace
 
-size_t linear_gemm_scratch(long long P, long long Q, long long R, bool scratch, int sms) {
-  const GemmPlan g = gemm_plan(P, Q, R, scratch, sms);
+size_t linear_gemm_scratch(long long P, long long Q, long long R, int sms) {
+  const GemmPlan g = gemm_plan(P, Q, R, true, sms);
   return g.pair && g.split > 1 ? (size_t)g.split * P * Q * 4 : 0;
 }
 
@@ -1028,7 +1029,8 @@ cudaError_t linear_gemm_launch(const GemmArgs& g, void* scratch, int sms, cudaSt
     return g.b_mn ? tile_launch<64, true, true, false>(g, s, stream)
                   : tile_launch<64, true, false, false>(g, s, stream);
   }
-  const GemmPlan f = gemm_plan(g.P, g.Q, g.R, scratch != nullptr, sms);
+  const bool plain = !g.bias && !g.res && !g.pre && g.act == kActNone;
+  const GemmPlan f = gemm_plan(g.P, g.Q, g.R, plain && scratch, sms);
   if (f.pair) return pair_launch(g, f.split, static_cast<float*>(scratch), sms, stream);
   if (f.bn == 64)
     return g.a_mn   ? tile_launch<64, false, true, true>(g, f.split, stream)

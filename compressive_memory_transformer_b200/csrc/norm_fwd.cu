@@ -112,11 +112,8 @@ template <typename T, int PIECE>
 cudaError_t by_width(const NormArgs& a, int kind, int sms, cudaStream_t stream) {
   if constexpr (PIECE * sizeof(T) == 16 && sizeof(T) == 2) {
     if (a.D > 2048) {
-      switch (norm_tpr(a.D, 32)) {
-        case 64: return launch<T, 64, PIECE, 32>(a, kind, sms, stream);
-        case 128: return launch<T, 128, PIECE, 32>(a, kind, sms, stream);
-        default: return launch<T, 256, PIECE, 32>(a, kind, sms, stream);
-      }
+      return norm_tpr(a.D, 32) == 128 ? launch<T, 128, PIECE, 32>(a, kind, sms, stream)
+                                      : launch<T, 256, PIECE, 32>(a, kind, sms, stream);
     }
   }
   switch (norm_tpr(a.D, 16)) {
