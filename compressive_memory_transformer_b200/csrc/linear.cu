@@ -950,8 +950,9 @@ struct GemmPlan {
 
 // Estimated time (us) of the tile kernel: a launch, and for every wave of blocks the time to
 // the first operands, the k-steps, which bring (128 + bn) x 128 bytes into an SM at its
-// share of L2 bandwidth, and the exchange of a split. Measured on 24 shapes from 100 x 512 x
-// 1024 to 16384 x 256 x 512 in all three storage orders; the estimates are within 15% there.
+// share of L2 bandwidth, and the exchange of a split. Against measured times of 34 products
+// that take this kernel, from 100 x 512 x 1024 to 16384 x 256 x 512 in all three storage orders,
+// the estimates lie between 12% below and 16% above, but for one of 5.8 us (7.5 estimated).
 double tile_time(int bn, int split, long long blocks, long long ksteps, int sms) {
   static const double step128 = 0.29, step64 = 0.20, step32 = 0.165, step16 = 0.15;
   static const double swap128[4] = {0.0, 2.3, 3.2, 4.4};  // for 1, 2, 4, 8 blocks
@@ -965,7 +966,10 @@ double tile_time(int bn, int split, long long blocks, long long ksteps, int sms)
 }
 
 // The same for the pair kernel: persistent, a k-step of 256 x 256 in 0.31 us, the last
-// tile's epilogue exposed; a split adds a launch and the partial sums' way through L2.
+// tile's epilogue exposed; a split adds a launch and the partial sums' way through L2. Up to
+// 8192 x 1024 x 1024 within 12% of measured times; 13 to 33% too low for ragged products (rows
+// off 128-byte lines and edge tiles cost more: 5003 x 1160 x 2056 24 us estimated, 32 taken)
+// and for long ones, whose clock is lower (32768 x 4096 x 1024 146 and 180).
 double pair_time(long long P, long long Q, int split, long long units, long long ksteps,
                  int sms) {
   const long long pairs = sms / 2, part = (ksteps + split - 1) / split;
@@ -1051,13 +1055,17 @@ constexpr int kActBlocks = 3;      // resident per SM
 constexpr int kActNarrowRows = 1024;
 
 // Columns of a block: 256 (a warp per row), or 32 for few rows (64 rows at a time), where
-// one block then takes all of them and the column sums need no second launch.
+// one block then takes all of them and the column sums need no second launch. Narrow and wide
+// with tanh gelu, us: 64 rows 2.4 and 4.2 (512 columns), 5.4 and 6.7 (16384); 512 rows 5.0 and
+// 4.8, 12.7 and 13.7; 1024 rows 8.0 and 5.4 (512), 8.2 and 6.3 (1408), 8.6 and 8.4 (4096), 23.1
+// and 22.5 (16384); 2048 rows 13.7 and 6.5, 47.7 and 41.8. Between 512 and 1024 rows the wide
+// form would save up to 2.6 us where columns are few.
 constexpr int act_cols(long long M) { return M <= kActNarrowRows ? 32 : 256; }
 
 // dpre = dy act'(pre), one 16-byte piece of a row per thread and step, and the column
 // sums of dpre before its rounding (fp32, one row of `part` per row chunk). HBM-bound:
-// dy and pre read once, dpre written once (16384 x 4096: 75 us = 5.4 TB/s with an
-// activation, 30 us = 4.5 TB/s for the sums alone).
+// dy and pre read once, dpre written once (16384 x 4096: 75 us = 5.4 TB/s with silu, 79 with
+// tanh gelu, 82 with gelu, 29 us = 4.6 TB/s for the sums alone).
 template <int ACT, int COLS>
 __global__ void __launch_bounds__(kActThreads, kActBlocks)
 act_grad_kernel(const __nv_bfloat16* __restrict__ dy, long long lddy,

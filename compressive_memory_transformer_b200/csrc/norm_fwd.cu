@@ -7,9 +7,10 @@
 //
 // b absent: r = alpha x, so that h is the plain norm of x. Everything between the loads
 // and the two stores is fp32 in registers; h is formed from the unrounded r.
-// HBM-bound: x and b read once, r and h written once (131072 x 1024 bf16: 170 us = 6.3 TB/s,
-// 98% of the measured copy bandwidth). A worker (threads of one row) asks
-// for its next row before it works on the present one.
+// HBM-bound: x and b read once, r and h written once (131072 x 1024 bf16: 167 us = 6.4 TB/s,
+// a plain copy's rate, launched back to back; 188 us = 5.7 TB/s as a pass of a program, with new
+// outputs and inputs each time). A worker (threads of one row) asks for its next row before
+// it works on the present one.
 #include "norm_common.cuh"
 
 namespace infini {
